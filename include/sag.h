@@ -81,6 +81,18 @@ typedef enum {
 
 typedef enum { SAG_F32 = 0, SAG_BF16 = 1 } sag_dtype;
 
+/* Activations of the dense layer and of group norm: z; max(z, 0) (NaN stays
+ * NaN, derivative 0 at 0); z > 0 ? z : slope z (derivative `slope` at 0); z
+ * times the normal distribution function (the erf form of GELU); z / (1 +
+ * exp(-z)).  `slope` is read by leaky ReLU alone. */
+typedef enum {
+    SAG_ACT_NONE = 0,
+    SAG_ACT_RELU = 1,
+    SAG_ACT_LEAKY_RELU = 2,
+    SAG_ACT_GELU = 3,
+    SAG_ACT_SILU = 4
+} sag_act;
+
 /* Normalisation of the adjacency (the values stored in the CSR).
  * SAG_NORM_GCN : entry (r, c) = 1 / sqrt(d_r * d_c), d = degrees of A + I
  *                (CAGNET page, background; Sylvie, "Forward Propagation").
@@ -591,6 +603,111 @@ sag_status sag_gemm_tn(int64_t M, int64_t N, const void* A1, int64_t lda1, int64
                        const void* B, int64_t ldb, const void* mask, int64_t ldmask,
                        float* C, int64_t ldc, float* colsum, sag_dtype dt,
                        void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dropout from a counter-based generator, its mask never stored (Srivastava
+ * et al., "Dropout", JMLR 2014, in the scaled form that leaves evaluation
+ * unchanged; the draws by Philox4x32-10 as for the low-bit messages).
+ *
+ * A sag_drop (host struct) says which mask: element j of row r is kept when
+ * its 16-bit draw is at least T = round(65536 p), kept values are scaled by
+ * 65536 / (65536 - T) and the others are 0 (whatever they held, NaN and
+ * infinities too).  p in [0, 1] is thus taken to the nearest 2^-16; T = 0
+ * draws nothing and T = 65536 keeps nothing.  The draw of element j of the
+ * row with stream id `node`: number j % 8 of the Philox4x32-10 block at
+ * counter (j / 8, node, call, 1), key (seed & 0xffffffff, seed >> 32), two
+ * draws per word, low half first.  node = nodes[r] (device int32, read as 32
+ * bits) or, where nodes is NULL, row0 + r, which has to stay below 2^32:
+ * with node ids for stream ids every partition drops the same elements of a
+ * node's row.  call = `call` plus, where call_dev is given, the word it points
+ * to (device uint32) when the kernel runs, modulo 2^32: a captured graph
+ * draws a new mask at each replay once the caller advances that word.
+ * The mask depends on nothing else (not on ld, dtype, width or which entry
+ * point applies it), so the backward pass recomputes it from the same
+ * description.  The struct is read during the call only. */
+typedef struct sag_drop {
+    float p;
+    uint32_t call;
+    uint64_t seed;
+    const uint32_t* call_dev;
+    const int32_t* nodes;
+    int64_t row0;
+} sag_drop;
+
+/* Out[r, j] = dropout(X)[r, j] (+ addend[r, j], nullable), in fp32 with one
+ * rounding to dt.  X, addend, Out: [n, d] of type dt.  The gradient of X is
+ * the same call on the gradient of Out.  Out may be X or the addend (same
+ * pointer and ld); any other overlap is not allowed.  Asynchronous. */
+sag_status sag_dropout(const void* X, int64_t ldx, int64_t n, int64_t d, sag_dtype dt, const sag_drop* drop,
+                       const void* addend, int64_t ld_add, void* Out, int64_t ldo, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense layer: the transform of a residual block, everything after the
+ * product in its epilogue (sag_gemm adds before its ReLU and knows no other
+ * activation, dropout or gradient).
+ *   Z = X W + b;  Out = R + dropout(act(Z))
+ * X: [M, K]; W: [K, N] row-major, ld N, no alignment needed; b: fp32[N],
+ * nullable; drop: nullable; R: [M, N], nullable; Z: [M, N], nullable (the
+ * backward call needs it unless act is SAG_ACT_NONE); Out: [M, N].  X, W, R,
+ * Z and Out of type dt, sums in fp32, each output rounded once (act sees the
+ * unrounded Z).  K, N >= 1; M may be 0.  Out may be R (same pointer and ld).
+ * K and N have no limit below 2^24. */
+size_t sag_dense_forward_workspace_bytes(int64_t M, int64_t K, int64_t N, sag_dtype dt);
+sag_status sag_dense_layer_forward(int64_t M, const void* X, int64_t ldx, int64_t K, const void* W, const float* b,
+                                   int64_t N, sag_act act, float slope, const sag_drop* drop, const void* R,
+                                   int64_t ldr, sag_dtype dt, void* Z, int64_t ldz, void* Out, int64_t ldo,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* Dense backward, with G the gradient of Out (R's gradient is G itself):
+ *   dZ = act'(Z) dropout(G);  dX = dZ W^T ([M, K], type dt, nullable);
+ *   dW = X^T dZ (fp32 [K, N], ld N, nullable);  db = column sums of dZ
+ *   (fp32[N], nullable).
+ * act, slope and drop have to be the forward's.  dW and db are held to fp32
+ * throughout for bf16 operands too; dX takes dZ rounded to dt. */
+size_t sag_dense_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, sag_dtype dt);
+sag_status sag_dense_layer_backward(int64_t M, const void* X, int64_t ldx, int64_t K, const void* W, int64_t N,
+                                    sag_act act, float slope, const sag_drop* drop, const void* Z, int64_t ldz,
+                                    const void* G, int64_t ldg, float* dW, float* db, void* dX, int64_t ldd,
+                                    sag_dtype dt, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation over the rows of each graph of a batch (Wu
+ * and He, "Group Normalization", ECCV 2018, channels last: a row holds a
+ * node's d channels, a graph's rows take the place of an image's pixels).
+ * Graph i owns rows seg[i] .. seg[i + 1] - 1 (device int64[n_seg + 1],
+ * ascending within [0, n_rows]; NULL with n_seg = 1: all rows); a group is
+ * d / groups adjacent channels.  groups = 1 normalises a graph as a whole,
+ * groups = d each channel of it on its own.
+ *   mean, var over the graph's rows and the group's channels (var divided by
+ *   the count);  rstd = 1 / sqrt(var + eps);
+ *   Out = act((X - mean) rstd w + b), w and b fp32[d] (NULL: 1 and 0).
+ * mean, rstd: fp32 [n_seg, groups], written; a graph without rows gets mean 0
+ * and rstd 1 / sqrt(eps).  Rows before the first graph and behind the last
+ * are left as they were in Out (and in dX).  Out may be X (same pointer and
+ * ld; the backward call then has no X).  d <= 1024 (fp32) or 2048 (bf16).
+ * Like a CSR's contents, seg is not checked: values outside [0, n_rows] are
+ * taken as the nearest end, and one that does not ascend leaves the results
+ * undefined. */
+size_t sag_group_norm_forward_workspace_bytes(int64_t n_rows, int64_t d, int64_t groups, int64_t n_seg,
+                                              sag_dtype dt);
+sag_status sag_group_norm_forward(const void* X, int64_t ldx, int64_t n_rows, int64_t d, int64_t groups,
+                                  const int64_t* seg, int64_t n_seg, const float* w, const float* b, float eps,
+                                  sag_act act, float slope, sag_dtype dt, void* Out, int64_t ldo, float* mean,
+                                  float* rstd, void* ws, size_t ws_bytes, void* stream);
+
+/* Group norm backward, from the forward's X, mean and rstd: with xhat = (X -
+ * mean) rstd, a = act'(xhat w + b) G and h = a w,
+ *   dw = sum of a xhat, db = sum of a over the rows of all graphs (fp32[d],
+ *   nullable);  dX = rstd (h - mean(h) - xhat mean(h xhat)), means over the
+ *   graph's rows and the group's channels ([n_rows, d], type dt, nullable;
+ *   may be G or X, same pointer and ld). */
+size_t sag_group_norm_backward_workspace_bytes(int64_t n_rows, int64_t d, int64_t groups, int64_t n_seg,
+                                               sag_dtype dt);
+sag_status sag_group_norm_backward(const void* X, int64_t ldx, int64_t n_rows, int64_t d, int64_t groups,
+                                   const int64_t* seg, int64_t n_seg, const float* w, const float* b, sag_act act,
+                                   float slope, const float* mean, const float* rstd, const void* G, int64_t ldg,
+                                   float* dw, float* db, void* dX, int64_t ldd, sag_dtype dt, void* ws,
+                                   size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement (opt-in, for benchmarks and profiling; not part of any

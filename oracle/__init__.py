@@ -33,10 +33,13 @@ What it computes, in float64 unless noted, and where each step is defined:
   textbook form since the pages print no formulas: per-entry LeakyReLU
   scores, a softmax over each row, the attention-weighted sum of the
   transformed rows, heads concatenated, and its backward pass.
+* ``block``      -- dropout from the counter-based generator, the dense layer
+  with bias, activation, dropout and residual, and group norm with an
+  activation over the rows of each graph, with their gradients.
 
 Where the pages leave a step open, the reading taken is stated in the
 docstring of the function that takes it.  Every function is pinned by tests
 under ``tests/`` that do not re-type its formulas: closed forms, invariants,
 brute force on tiny inputs and finite differences.
 """
-from . import csr, gat, layers, lowbit, native  # noqa: F401
+from . import block, csr, gat, layers, lowbit, native  # noqa: F401

@@ -22,6 +22,7 @@ SAG_F32, SAG_BF16 = 0, 1
 SAG_NORM_GCN, SAG_NORM_MEAN, SAG_NORM_NONE = 0, 1, 2
 SAG_SYMMETRIZE, SAG_SELF_LOOPS = 1, 2
 SAG_LAYER_FUSED = 1
+SAG_ACT_NONE, SAG_ACT_RELU, SAG_ACT_LEAKY_RELU, SAG_ACT_GELU, SAG_ACT_SILU = 0, 1, 2, 3, 4
 
 
 class SagCsr(ctypes.Structure):
@@ -36,7 +37,16 @@ class SagCsr(ctypes.Structure):
     ]
 
 
+class SagDrop(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_float), ("call", u32), ("seed", ctypes.c_uint64),
+        ("call_dev", vp), ("nodes", vp), ("row0", i64),
+    ]
+
+
 PCSR = P(SagCsr)
+PDROP = P(SagDrop)
+f32 = ctypes.c_float
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -91,6 +101,19 @@ SIGNATURES = {
     "sag_gemm_tn_workspace_bytes": (sz, [i64, i64, i64, cint]),
     "sag_gemm_tn": (cint, [i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp, i64,
                            vp, cint, vp, sz, vp]),
+    "sag_dropout": (cint, [vp, i64, i64, i64, cint, PDROP, vp, i64, vp, i64, vp]),
+    "sag_dense_forward_workspace_bytes": (sz, [i64, i64, i64, cint]),
+    "sag_dense_layer_forward": (cint, [i64, vp, i64, i64, vp, vp, i64, cint, f32, PDROP, vp, i64, cint, vp, i64,
+                                       vp, i64, vp, sz, vp]),
+    "sag_dense_backward_workspace_bytes": (sz, [i64, i64, i64, cint]),
+    "sag_dense_layer_backward": (cint, [i64, vp, i64, i64, vp, i64, cint, f32, PDROP, vp, i64, vp, i64, vp, vp,
+                                        vp, i64, cint, vp, sz, vp]),
+    "sag_group_norm_forward_workspace_bytes": (sz, [i64, i64, i64, i64, cint]),
+    "sag_group_norm_forward": (cint, [vp, i64, i64, i64, i64, vp, i64, vp, vp, f32, cint, f32, cint, vp, i64, vp,
+                                      vp, vp, sz, vp]),
+    "sag_group_norm_backward_workspace_bytes": (sz, [i64, i64, i64, i64, cint]),
+    "sag_group_norm_backward": (cint, [vp, i64, i64, i64, i64, vp, i64, vp, vp, cint, f32, vp, vp, vp, i64, vp, vp,
+                                       vp, i64, cint, vp, sz, vp]),
     "sag_trace_enable": (cint, [cint]),
     "sag_trace_count": (i64, []),
     "sag_trace_get": (cint, [i64, ctypes.c_char_p, sz, P(ctypes.c_float), P(i64), P(i64)]),

@@ -21,7 +21,7 @@
 // a time (one 16-byte bf16 vector or two fp32 vectors), so that a lane's
 // codes are b whole bytes: element j of the row occupies bits
 // [b j, b j + b) of the row's codes, little-endian.
-#include "common.h"
+#include "philox.h"
 #include "trace.h"
 
 // Every fp32 step below is rounded on its own: no multiply-add contraction
@@ -32,28 +32,6 @@
 
 namespace sag {
 namespace {
-
-constexpr uint32_t kPhiloxM0 = 0xD2511F53u, kPhiloxM1 = 0xCD9E8D57u;
-constexpr uint32_t kPhiloxW0 = 0x9E3779B9u, kPhiloxW1 = 0xBB67AE85u;
-
-// Philox4x32 with 10 rounds: c is the counter in and the block out.  Each
-// round's two 32 x 32 -> 64-bit products are taken whole, so one
-// instruction gives both halves of each.
-__device__ __forceinline__ void philox4x32_10(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
-#pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t p0 = static_cast<uint64_t>(kPhiloxM0) * c[0];
-        const uint64_t p1 = static_cast<uint64_t>(kPhiloxM1) * c[2];
-        const uint32_t n0 = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
-        const uint32_t n2 = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
-        c[0] = n0;
-        c[1] = static_cast<uint32_t>(p1);
-        c[2] = n2;
-        c[3] = static_cast<uint32_t>(p0);
-        k0 += kPhiloxW0;
-        k1 += kPhiloxW1;
-    }
-}
 
 // The eight elements [8g, 8g + 8) of a row as fp32 (elements past d read
 // as 0).  Loads are whole 16-byte vectors: the vector that holds the row's

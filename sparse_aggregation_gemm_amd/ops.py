@@ -770,6 +770,287 @@ def gemm_tn(A1, B, A2=None, mask=None, want_colsum=True):
     return (C, cs) if want_colsum else C
 
 
+# ---- dropout, dense layer, group norm -----------------------------------------------------
+
+_ACT = {"none": L.SAG_ACT_NONE, "relu": L.SAG_ACT_RELU, "leaky_relu": L.SAG_ACT_LEAKY_RELU,
+        "gelu": L.SAG_ACT_GELU, "silu": L.SAG_ACT_SILU}
+
+
+def _act_code(act: str) -> int:
+    if act not in _ACT:
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(_ACT)})")
+    return _ACT[act]
+
+
+def _need(what: str, t, shape, dtype, device) -> None:
+    """ValueError (TypeError for the element type) unless t, when given, is a
+    tensor of this shape, type and device."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}; the call takes {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}; the call takes {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}; the call runs on {device}")
+
+
+def _need_rows_2d(what: str, t) -> None:
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    if t.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+def _row_vec(what: str, t, n: int, device):
+    """A contiguous fp32[n] parameter, or None."""
+    _need(what, t, (n,), torch.float32, device)
+    return None if t is None else t.contiguous()
+
+
+class _on:
+    """Makes `device` the current one for a launch on it."""
+
+    def __init__(self, device):
+        self.device = device
+        self.back = None
+
+    def __enter__(self):
+        if self.device.type == "cuda" and self.device.index is not None \
+                and torch.cuda.current_device() != self.device.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+@dataclass(frozen=True)
+class Drop:
+    """A dropout mask (sag_drop), never stored: probability p of dropping
+    (taken to the nearest 2^-16), the generator's seed and call number, the
+    stream ids of the rows (nodes: int32 [rows] on the device; None: row0 + r)
+    and, for captured graphs, a device word (counter: int32 or uint32 [1])
+    added to `call` when the kernel runs."""
+    p: float
+    seed: int
+    call: int = 0
+    nodes: torch.Tensor | None = None
+    row0: int = 0
+    counter: torch.Tensor | None = None
+
+
+def _drop(drop: Drop | None, rows: int, device):
+    """(ctypes pointer or None) for `rows` rows."""
+    if drop is None:
+        return None
+    if not 0.0 <= drop.p <= 1.0:
+        raise ValueError("dropout p must lie in [0, 1]")
+    if drop.nodes is not None:
+        _need("dropout nodes", drop.nodes, (rows,), torch.int32, device)
+        if not drop.nodes.is_contiguous():
+            raise ValueError("dropout nodes must be contiguous")
+    if drop.counter is not None:
+        if drop.counter.dtype not in (torch.int32, torch.uint32) or drop.counter.numel() != 1 \
+                or drop.counter.device != device:
+            raise ValueError("the dropout counter must be one int32 or uint32 on the call's device")
+    return ctypes.byref(L.SagDrop(drop.p, drop.call & 0xFFFFFFFF, drop.seed & (2 ** 64 - 1), _ptr(drop.counter),
+                                  _ptr(drop.nodes), drop.row0))
+
+
+def dropout(X, drop: Drop, addend=None, Out=None):
+    """sag_dropout: Out = dropout(X) (+ addend).  The gradient of X is the same
+    call on the gradient of Out.  Out may be X or the addend."""
+    _need_rows_2d("dropout X", X)
+    _need("dropout addend", addend, X.shape, X.dtype, X.device)
+    _need("dropout Out", Out, X.shape, X.dtype, X.device)
+    if Out is None:
+        Out = empty_dense(X.shape[0], X.shape[1], X.dtype, X.device)
+    d = _drop(drop, X.shape[0], X.device)
+    with _on(X.device):
+        st = L.lib().sag_dropout(_ptr(X), _ld(X), X.shape[0], X.shape[1], dtype_code(X.dtype), d, _ptr(addend),
+                                 _ld(addend) if addend is not None else 0, _ptr(Out), _ld(Out), _stream(X.device))
+    L.check("sag_dropout", st)
+    return Out
+
+
+@dataclass
+class DenseCtx:
+    """What the dense layer's forward hands to its backward."""
+    X: torch.Tensor
+    W: torch.Tensor
+    act: str = "none"
+    slope: float = 0.01
+    drop: Drop | None = None
+
+
+def dense_layer_forward(X, W, b=None, act="relu", slope=0.01, drop: Drop | None = None, residual=None, want_z=None,
+                        Out=None, Z=None, ws=None):
+    """sag_dense_layer_forward: Out = residual + dropout(act(X W + b)).  Returns
+    (Out, Z, ctx); Z = X W + b is written when want_z (default: when the
+    backward needs it, i.e. act is not "none").  Out may be the residual."""
+    _need_rows_2d("dense_layer_forward X", X)
+    dev, M, K = X.device, X.shape[0], X.shape[1]
+    _need_rows_2d("dense_layer_forward W", W)
+    N = W.shape[1]
+    _need("dense_layer_forward W", W, (K, N), X.dtype, dev)
+    b = _row_vec("dense_layer_forward b", b, N, dev)
+    _need("dense_layer_forward residual", residual, (M, N), X.dtype, dev)
+    _need("dense_layer_forward Out", Out, (M, N), X.dtype, dev)
+    _need("dense_layer_forward Z", Z, (M, N), X.dtype, dev)
+    code = _act_code(act)
+    d = _drop(drop, M, dev)
+    if want_z is None:
+        want_z = act != "none"
+    lib = L.lib()
+    dt = dtype_code(X.dtype)
+    W = W.contiguous()
+    if Out is None:
+        Out = empty_dense(M, N, X.dtype, dev)
+    if not want_z:
+        Z = None
+    elif Z is None:
+        Z = empty_dense(M, N, X.dtype, dev)
+    nws = lib.sag_dense_forward_workspace_bytes(M, K, N, dt)
+    if ws is None or ws.numel() < nws:
+        ws = _ws(nws, dev)
+    with _on(dev):
+        st = lib.sag_dense_layer_forward(M, _ptr(X), _ld(X), K, _ptr(W), _ptr(b), N, code, float(slope), d,
+                                         _ptr(residual), _ld(residual) if residual is not None else 0, dt, _ptr(Z),
+                                         _ld(Z) if Z is not None else 0, _ptr(Out), _ld(Out), _ptr(ws), ws.numel(),
+                                         _stream(dev))
+    L.check("sag_dense_layer_forward", st)
+    return Out, Z, DenseCtx(X, W, act, float(slope), drop)
+
+
+def dense_layer_backward(ctx: DenseCtx, Z, G_out, want_dX=True, want_db=True, dX=None, ws=None):
+    """sag_dense_layer_backward: returns (dW, db, dX) from the gradient of Out
+    (which is also the residual's).  Z may be None when the activation is
+    "none"."""
+    X, W = ctx.X, ctx.W
+    _need_rows_2d("dense_layer_backward X", X)
+    dev, M, K, N = X.device, X.shape[0], X.shape[1], W.shape[1]
+    _need("dense_layer_backward W", W, (K, N), X.dtype, dev)
+    code = _act_code(ctx.act)
+    if ctx.act == "none":
+        Z = None
+    elif Z is None:
+        raise ValueError("dense_layer_backward needs Z for this activation")
+    _need("dense_layer_backward Z", Z, (M, N), X.dtype, dev)
+    _need("dense_layer_backward G_out", G_out, (M, N), X.dtype, dev)
+    _need("dense_layer_backward dX", dX, (M, K), X.dtype, dev)
+    d = _drop(ctx.drop, M, dev)
+    lib = L.lib()
+    dt = dtype_code(X.dtype)
+    W = W.contiguous()
+    dW = torch.empty((K, N), dtype=torch.float32, device=dev)
+    db = torch.empty(N, dtype=torch.float32, device=dev) if want_db else None
+    if not want_dX:
+        dX = None
+    elif dX is None:
+        dX = empty_dense(M, K, X.dtype, dev)
+    nws = lib.sag_dense_backward_workspace_bytes(M, K, N, dt)
+    if ws is None or ws.numel() < nws:
+        ws = _ws(nws, dev)
+    with _on(dev):
+        st = lib.sag_dense_layer_backward(M, _ptr(X), _ld(X), K, _ptr(W), N, code, ctx.slope, d, _ptr(Z),
+                                          _ld(Z) if Z is not None else 0, _ptr(G_out), _ld(G_out), _ptr(dW), _ptr(db),
+                                          _ptr(dX), _ld(dX) if dX is not None else 0, dt, _ptr(ws), ws.numel(),
+                                          _stream(dev))
+    L.check("sag_dense_layer_backward", st)
+    return dW, db, dX
+
+
+@dataclass
+class GroupNormCtx:
+    """What group norm's forward hands to its backward (mean and rstd: fp32
+    [graphs, groups])."""
+    X: torch.Tensor
+    groups: int
+    weight: torch.Tensor | None
+    bias: torch.Tensor | None
+    seg: torch.Tensor | None
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    act: str = "none"
+    slope: float = 0.01
+
+
+def _norm_args(what, X, groups, weight, bias, seg):
+    _need_rows_2d(f"{what} X", X)
+    dev, d = X.device, X.shape[1]
+    if groups < 1 or d % groups:
+        raise ValueError(f"{what}: groups must divide the width {d}")
+    weight = _row_vec(f"{what} weight", weight, d, dev)
+    bias = _row_vec(f"{what} bias", bias, d, dev)
+    if seg is None:
+        return weight, bias, None, 1
+    if seg.dim() != 1 or seg.numel() < 1:
+        raise ValueError(f"{what}: seg must be 1-D with one entry more than graphs")
+    _need(f"{what} seg", seg, seg.shape, torch.int64, dev)
+    return weight, bias, seg.contiguous(), seg.numel() - 1
+
+
+def group_norm_forward(X, groups=1, weight=None, bias=None, seg=None, eps=1e-5, act="none", slope=0.01, Out=None,
+                       ws=None):
+    """sag_group_norm_forward: Out = act(groupnorm(X) weight + bias) with the
+    statistics of each graph (rows seg[i] .. seg[i + 1] - 1; seg None: one
+    graph) and group of adjacent channels.  Returns (Out, ctx).  A fresh Out
+    has zeros in the rows of no graph.  Out may be X."""
+    weight, bias, seg, n_seg = _norm_args("group_norm_forward", X, groups, weight, bias, seg)
+    dev, n, d = X.device, X.shape[0], X.shape[1]
+    _need("group_norm_forward Out", Out, X.shape, X.dtype, dev)
+    code = _act_code(act)
+    lib = L.lib()
+    dt = dtype_code(X.dtype)
+    if Out is None:
+        Out = empty_dense(n, d, X.dtype, dev, fill=None if seg is None else 0.0)
+    mean = torch.empty((n_seg, groups), dtype=torch.float32, device=dev)
+    rstd = torch.empty((n_seg, groups), dtype=torch.float32, device=dev)
+    nws = lib.sag_group_norm_forward_workspace_bytes(n, d, groups, n_seg, dt)
+    if ws is None or ws.numel() < nws:
+        ws = _ws(nws, dev)
+    with _on(dev):
+        st = lib.sag_group_norm_forward(_ptr(X), _ld(X), n, d, groups, _ptr(seg), n_seg, _ptr(weight), _ptr(bias),
+                                        float(eps), code, float(slope), dt, _ptr(Out), _ld(Out), _ptr(mean), _ptr(rstd),
+                                        _ptr(ws), ws.numel(), _stream(dev))
+    L.check("sag_group_norm_forward", st)
+    return Out, GroupNormCtx(X, groups, weight, bias, seg, mean, rstd, act, float(slope))
+
+
+def group_norm_backward(ctx: GroupNormCtx, G_out, want_dX=True, dX=None, ws=None):
+    """sag_group_norm_backward: returns (dweight, dbias, dX).  A fresh dX has
+    zeros in the rows of no graph.  dX may be G_out."""
+    X = ctx.X
+    weight, bias, seg, n_seg = _norm_args("group_norm_backward", X, ctx.groups, ctx.weight, ctx.bias, ctx.seg)
+    dev, n, d = X.device, X.shape[0], X.shape[1]
+    _need("group_norm_backward G_out", G_out, X.shape, X.dtype, dev)
+    _need("group_norm_backward dX", dX, X.shape, X.dtype, dev)
+    _need("group_norm_backward mean", ctx.mean, (n_seg, ctx.groups), torch.float32, dev)
+    _need("group_norm_backward rstd", ctx.rstd, (n_seg, ctx.groups), torch.float32, dev)
+    code = _act_code(ctx.act)
+    lib = L.lib()
+    dt = dtype_code(X.dtype)
+    mean, rstd = ctx.mean.contiguous(), ctx.rstd.contiguous()
+    dw = torch.empty(d, dtype=torch.float32, device=dev)
+    dv = torch.empty(d, dtype=torch.float32, device=dev)
+    if not want_dX:
+        dX = None
+    elif dX is None:
+        dX = empty_dense(n, d, X.dtype, dev, fill=None if seg is None else 0.0)
+    nws = lib.sag_group_norm_backward_workspace_bytes(n, d, ctx.groups, n_seg, dt)
+    if ws is None or ws.numel() < nws:
+        ws = _ws(nws, dev)
+    with _on(dev):
+        st = lib.sag_group_norm_backward(_ptr(X), _ld(X), n, d, ctx.groups, _ptr(seg), n_seg, _ptr(weight), _ptr(bias),
+                                         code, float(ctx.slope), _ptr(mean), _ptr(rstd), _ptr(G_out), _ld(G_out),
+                                         _ptr(dw), _ptr(dv), _ptr(dX), _ld(dX) if dX is not None else 0, dt, _ptr(ws),
+                                         ws.numel(), _stream(dev))
+    L.check("sag_group_norm_backward", st)
+    return dw, dv, dX
+
+
 def trace_enable(on: bool = True) -> None:
     """sag_trace_enable: HIP-event timing of every internal operation."""
     L.check("sag_trace_enable", L.lib().sag_trace_enable(int(on)))
