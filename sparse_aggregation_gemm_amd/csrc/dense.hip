@@ -24,6 +24,9 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+// (a vector type, not the uint4 class, whose conditional copies go through
+// private memory)
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kBM = 128;
@@ -43,39 +46,41 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t bid, int64_t total) {
 
 // Zeroes elements >= n of a vector of T.
 template <class T>
-__device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (sizeof(T) == 4) {
+__device__ __forceinline__ u32x4_t keep_first(u32x4_t v, int n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = e < n ? w[e] : 0u;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e >= n) w[e / 2] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) v[e] = e < n ? v[e] : 0u;
+        else v[e] = 2 * e + 1 < n ? v[e] : (2 * e < n ? v[e] & 0xffffu : 0u);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return v;
 }
+__device__ __forceinline__ u32x4_t load16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
+__device__ __forceinline__ void store16(void* p, u32x4_t v) { *reinterpret_cast<u32x4_t*>(p) = v; }
+__device__ __forceinline__ uint4 as_uint4(u32x4_t v) { return make_uint4(v[0], v[1], v[2], v[3]); }
 
 // Eight consecutive elements of a row: loads (columns past n read as they
 // are: the pitch covers the last vector, a vector past it is not read),
 // values and stores.
 template <class T>
 struct Eight {
-    uint4 v[sizeof(T) / 2];
+    u32x4_t v[sizeof(T) / 2];
     __device__ __forceinline__ void load(const T* p, int live) {
-        v[0] = *reinterpret_cast<const uint4*>(p);
-        if constexpr (sizeof(T) == 4) v[1] = live > 4 ? *reinterpret_cast<const uint4*>(p + 4) : make_uint4(0, 0, 0, 0);
+        v[0] = load16(p);
+        if constexpr (sizeof(T) == 4) {
+            v[1] = u32x4_t{0u, 0u, 0u, 0u};
+            if (live > 4) v[1] = load16(p + 4);
+        }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
-        unpack<T>(v[0], f);
-        if constexpr (sizeof(T) == 4) unpack<T>(v[1], f + 4);
+        unpack<T>(as_uint4(v[0]), f);
+        if constexpr (sizeof(T) == 4) unpack<T>(as_uint4(v[1]), f + 4);
     }
     static __device__ __forceinline__ void put(T* p, const float (&f)[8], int live) {
         if constexpr (sizeof(T) == 2) {
-            store_vals<T>(p, f, live);
+            store_first<T>(p, f, live);
         } else {
-            store_vals<T>(p, f, live < 4 ? live : 4);
-            if (live > 4) store_vals<T>(p + 4, f + 4, live - 4);
+            store_first<T>(p, f, live);
+            if (live > 4) store_first<T>(p + 4, f + 4, live - 4);
         }
     }
 };
@@ -118,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
     const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
     const int64_t m0 = tile / p.n_blk * kBM, n0 = tile % p.n_blk * BN;
 
-    uint4 ra[UA], rb[UB];
+    u32x4_t ra[UA], rb[UB];
     const int64_t last = (p.K + V - 1) / V * V - V;
     auto load = [&](int64_t k0) {
 #pragma unroll
@@ -126,27 +131,27 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
             const int q = t + i * kThreads, r = q >> 3, u = q & 7;
             const int64_t row = m0 + r < p.M ? m0 + r : p.M - 1;
             const int64_t k = k0 + u * V;
-            ra[i] = *reinterpret_cast<const uint4*>(p.a + row * p.lda + (k < last ? k : last));
+            ra[i] = load16(p.a + row * p.lda + (k < last ? k : last));
         }
 #pragma unroll
         for (int i = 0; i < UB; ++i) {
             const int q = t + i * kThreads, r = q >> 3, u = q & 7;
-            rb[i] = *reinterpret_cast<const uint4*>(p.bp + (n0 + r) * p.Kt + k0 + u * V);
+            rb[i] = load16(p.bp + (n0 + r) * p.Kt + k0 + u * V);
         }
     };
     auto store = [&](int64_t k0) {
+        const bool edge = k0 + CK > p.K;
 #pragma unroll
         for (int i = 0; i < UA; ++i) {
             const int q = t + i * kThreads, r = q >> 3, u = q & 7;
             const int64_t left = p.K - k0 - u * V;
-            uint4 v = ra[i];
-            if (left < V) v = keep_first<T>(v, left > 0 ? static_cast<int>(left) : 0);
-            *reinterpret_cast<uint4*>(As + r * kRowB + ((u ^ swz(r)) << 4)) = v;
+            store16(As + r * kRowB + ((u ^ swz(r)) << 4),
+                    edge ? keep_first<T>(ra[i], left < V ? (left > 0 ? static_cast<int>(left) : 0) : V) : ra[i]);
         }
 #pragma unroll
         for (int i = 0; i < UB; ++i) {
             const int q = t + i * kThreads, r = q >> 3, u = q & 7;
-            *reinterpret_cast<uint4*>(Bs + r * kRowB + ((u ^ swz(r)) << 4)) = rb[i];
+            store16(Bs + r * kRowB + ((u ^ swz(r)) << 4), rb[i]);
         }
     };
     f32x16_t acc[MB][NB];
@@ -164,16 +169,16 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
         if (k0 + CK < p.Kt) load(k0 + CK);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            uint4 a[MB], b[NB];
+            u32x4_t a[MB], b[NB];
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
                 const int r = (wm * MB + i) * 32 + l32;
-                a[i] = *reinterpret_cast<const uint4*>(As + r * kRowB + (((2 * s + h) ^ swz(r)) << 4));
+                a[i] = load16(As + r * kRowB + (((2 * s + h) ^ swz(r)) << 4));
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const int r = (wn * NB + j) * 32 + l32;
-                b[j] = *reinterpret_cast<const uint4*>(Bs + r * kRowB + (((2 * s + h) ^ swz(r)) << 4));
+                b[j] = load16(Bs + r * kRowB + (((2 * s + h) ^ swz(r)) << 4));
             }
 #pragma unroll
             for (int i = 0; i < MB; ++i)
@@ -391,7 +396,7 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
     if (dX && M > 0) {
         NnArgs<T> p{};
         p.a = hi; p.lda = ldh; p.M = M; p.K = N; p.N = K;
-        p.drop = DropArgs{0u, 1.f, 0u, 0u, 0u, 0u, nullptr, nullptr};
+        p.drop = DropArgs{};
         p.out = dX; p.ldo = ldd;
         SAG_TRY(nn_run<T>("dense_dx", SAG_ACT_NONE, p, W, 1, N, static_cast<T*>(w.bp), dt, s));
     }

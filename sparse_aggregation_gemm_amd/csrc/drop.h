@@ -18,7 +18,8 @@
 namespace sag {
 
 struct DropArgs {
-    uint32_t T;                 // 0: everything is kept
+    uint32_t T;                 // 0: everything is kept and nothing below is read
+    uint32_t last;              // 65536 T - 1: a draw in a word's high half is dropped up to here
     float scale;                // 65536 / (65536 - T); 0 when T = 65536
     uint32_t key0, key1, call, row0;
     const uint32_t* call_dev;   // nullable: added to call when the kernel runs
@@ -36,16 +37,18 @@ struct DropArgs {
         w[3] = 1u;
         philox4x32_10(w, key0, key1);
     }
-    // x of column e (of the eight) after dropout; a dropped NaN or infinity is 0.
+    // x of column e (of the eight) after dropout; a dropped NaN or infinity
+    // is 0.  (A draw u in the high half and anything below it: u < T where
+    // the word is at most 65536 T - 1, so the odd columns need no shift.)
     __device__ __forceinline__ float apply(float x, const uint32_t (&w)[4], int e) const {
-        const uint32_t u = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-        return u >= T ? x * scale : 0.f;
+        const uint32_t u = (e & 1) ? w[e / 2] : w[e / 2] << 16;
+        return u > last ? x * scale : 0.f;
     }
 };
 
 // Checks a caller's sag_drop (null: no dropout) for `rows` rows.
 inline sag_status make_drop(const char* who, const sag_drop* d, int64_t rows, DropArgs* out) {
-    *out = DropArgs{0u, 1.f, 0u, 0u, 0u, 0u, nullptr, nullptr};
+    *out = DropArgs{};
     if (!d) return SAG_OK;
     if (!(d->p >= 0.f && d->p <= 1.f)) return fail(SAG_E_INVALID, std::string(who) + ": dropout p outside [0, 1]");
     const uint32_t T = static_cast<uint32_t>(std::floor(static_cast<double>(d->p) * 65536.0 + 0.5));
@@ -53,6 +56,7 @@ inline sag_status make_drop(const char* who, const sag_drop* d, int64_t rows, Dr
     if (!d->nodes && (d->row0 < 0 || d->row0 > (int64_t{1} << 32) - rows))
         return fail(SAG_E_INVALID, std::string(who) + ": dropout row ids outside 32 bits");
     out->T = T;
+    out->last = (T << 16) - 1u;   // T = 65536: all ones
     out->scale = T == 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - T));
     out->key0 = static_cast<uint32_t>(d->seed);
     out->key1 = static_cast<uint32_t>(d->seed >> 32);
@@ -63,18 +67,59 @@ inline sag_status make_drop(const char* who, const sag_drop* d, int64_t rows, Dr
     return SAG_OK;
 }
 
+// Stores the first n (1 to V) of a vector's worth of values at p, 16-byte
+// aligned; written out so that the values stay in registers.
+template <class T>
+__device__ __forceinline__ void store_first(T* p, const float* f, int n) {
+    constexpr int V = Vec<T>::N;
+    if (n >= V) {
+        store_vals<T>(p, f, V);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < n) p[e] = from_f32<T>(f[e]);
+    }
+}
+
 inline bool act_ok(sag_act a) { return a >= SAG_ACT_NONE && a <= SAG_ACT_SILU; }
 
-constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+// The normal distribution function, through its tail: for a >= 0
+//   1 - Phi(a) = exp(-a^2 / 2) t P(t),  t = 1 / (1 + 0.3 a),
+// where t P(t) stands for half the scaled complementary error function.  P
+// (degree 7) is a least-maximum fit of relative error 1.5e-7 on [0, 14],
+// beyond which the exponential is 0 in fp32 (Lawson's reweighted least
+// squares on 12,000 points).  The tail keeps its relative accuracy, and the
+// exponential is also the density that the derivative needs.  The library's
+// erfcf, which branches by range, took 1.3 ms against 0.9 ms for this in the
+// gradient pass over 2.45M x 256 bf16 (a pass of 5.0 GB).
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, fabsf(z), 1.f));
+    e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);   // exp(-z^2 / 2)
+    float p = 0.0356758525f;
+    p = fmaf(p, t, -0.157207547f);
+    p = fmaf(p, t, 0.206361131f);
+    p = fmaf(p, t, -0.0536906036f);
+    p = fmaf(p, t, 0.128565293f);
+    p = fmaf(p, t, 0.0999123772f);
+    p = fmaf(p, t, 0.120754137f);
+    p = fmaf(p, t, 0.119629287f);
+    const float q = p * t * e;
+    return z < 0.f ? q : 1.f - q;
+}
 
-// act(z) in fp32.  ReLU keeps NaN; GELU is z times the normal distribution
-// function, through erfc so that the left tail keeps its relative accuracy.
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+
+// act(z) in fp32.  ReLU keeps NaN.
 template <int ACT>
 __device__ __forceinline__ float act_value(float z, float slope) {
     if constexpr (ACT == SAG_ACT_RELU) return z < 0.f ? 0.f : z;
     else if constexpr (ACT == SAG_ACT_LEAKY_RELU) return z > 0.f ? z : z * slope;
-    else if constexpr (ACT == SAG_ACT_GELU) return 0.5f * z * erfcf(-kSqrtHalf * z);
-    else if constexpr (ACT == SAG_ACT_SILU) return z / (1.f + expf(-z));
+    else if constexpr (ACT == SAG_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    } else if constexpr (ACT == SAG_ACT_SILU) return z * sigmoid(z);
     else return z;
 }
 
@@ -83,11 +128,13 @@ template <int ACT>
 __device__ __forceinline__ float act_grad(float z, float slope) {
     if constexpr (ACT == SAG_ACT_RELU) return z > 0.f ? 1.f : 0.f;
     else if constexpr (ACT == SAG_ACT_LEAKY_RELU) return z > 0.f ? 1.f : slope;
-    else if constexpr (ACT == SAG_ACT_GELU)
-        return 0.5f * erfcf(-kSqrtHalf * z) + z * (kInvSqrt2Pi * expf(-0.5f * z * z));
-    else if constexpr (ACT == SAG_ACT_SILU) {
-        const float e = 1.f / (1.f + expf(-z));
-        return e * (1.f + z * (1.f - e));
+    else if constexpr (ACT == SAG_ACT_GELU) {
+        float e;
+        const float c = normal_cdf(z, e);
+        return fmaf(z * 0.39894228040143268f, e, c);             // Phi + z phi
+    } else if constexpr (ACT == SAG_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * fmaf(z, 1.f - s, 1.f);
     } else return 1.f;
 }
 

@@ -78,12 +78,14 @@ __global__ __launch_bounds__(kThreads) void dropout_rows(Args a) {
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         if (base + threadIdx.x + i * kThreads >= a.total) continue;
-        uint32_t w[4];
-        a.drop.draws(node[i], g[i], call, w);
         float f[8];
         unpack_unit<T>(xv[i], f);
+        if (a.drop.T) {
+            uint32_t w[4];
+            a.drop.draws(node[i], g[i], call, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = a.drop.apply(f[e], w, e);
+            for (int e = 0; e < 8; ++e) f[e] = a.drop.apply(f[e], w, e);
+        }
         if constexpr (ADD) {
             float h[8];
             unpack_unit<T>(av[i], h);
@@ -94,10 +96,10 @@ __global__ __launch_bounds__(kThreads) void dropout_rows(Args a) {
         const int live = static_cast<int>(a.d - j0 < 8 ? a.d - j0 : 8);
         T* p = static_cast<T*>(a.out) + row[i] * a.ldo + j0;
         if constexpr (sizeof(T) == 2) {
-            store_vals<T>(p, f, live);
+            store_first<T>(p, f, live);
         } else {
-            store_vals<T>(p, f, live < 4 ? live : 4);
-            if (live > 4) store_vals<T>(p + 4, f + 4, live - 4);
+            store_first<T>(p, f, live);
+            if (live > 4) store_first<T>(p + 4, f + 4, live - 4);
         }
     }
 }

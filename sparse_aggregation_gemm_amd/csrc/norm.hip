@@ -330,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply(NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     f[e] = act_value<ACT>((f[e] - k.mean[e]) * k.rstd[e] * k.w[e] + k.v[e], a.slope);
-                store_vals<T>(out + ri * a.ldo, f, nc);
+                store_first<T>(out + ri * a.ldo, f, nc);
             }
         }
     });
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_apply(NormArgs a) {
                     const float t = grad_a<ACT>(f[e], q[e], k.mean[e], k.rstd[e], k.w[e], k.v[e], a.slope, xh);
                     f[e] = k.rstd[e] * (t * k.w[e] - m0[e] - xh * m1[e]);
                 }
-                store_vals<T>(out + ri * a.ldo, f, nc);
+                store_first<T>(out + ri * a.ldo, f, nc);
             }
         }
     });
