@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
             for (int e = 0; e < 8; ++e) y[e] += bias[e];
             if (p.z) Eight<T>::put(p.z + row * p.ldz + col, y, live);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = act_value<ACT>(y[e], p.slope);
+            for (int e = 0; e < 8; ++e) y[e] = act_value<ACT, T>(y[e], p.slope);
             if constexpr (DROP) {
                 uint32_t dw[4];
                 p.drop.draws(p.drop.node_of(row), static_cast<uint32_t>(col >> 3), call, dw);

@@ -67,13 +67,24 @@ inline sag_status make_drop(const char* who, const sag_drop* d, int64_t rows, Dr
     return SAG_OK;
 }
 
+// Two fp32 values as packed bf16 (round to nearest even, one instruction).
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    const f32x2_t v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
 // Stores the first n (1 to V) of a vector's worth of values at p, 16-byte
 // aligned; written out so that the values stay in registers.
 template <class T>
 __device__ __forceinline__ void store_first(T* p, const float* f, int n) {
     constexpr int V = Vec<T>::N;
     if (n >= V) {
-        store_vals<T>(p, f, V);
+        if constexpr (V == 8)
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+        else
+            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -83,42 +94,53 @@ __device__ __forceinline__ void store_first(T* p, const float* f, int n) {
 
 inline bool act_ok(sag_act a) { return a >= SAG_ACT_NONE && a <= SAG_ACT_SILU; }
 
-// The normal distribution function, through its tail: for a >= 0
-//   1 - Phi(a) = exp(-a^2 / 2) t P(t),  t = 1 / (1 + 0.3 a),
-// where t P(t) stands for half the scaled complementary error function.  P
-// (degree 7) is a least-maximum fit of relative error 1.5e-7 on [0, 14],
-// beyond which the exponential is 0 in fp32 (Lawson's reweighted least
-// squares on 12,000 points).  The tail keeps its relative accuracy, and the
-// exponential is also the density that the derivative needs.  The library's
-// erfcf, which branches by range, took 1.3 ms against 0.9 ms for this in the
-// gradient pass over 2.45M x 256 bf16 (a pass of 5.0 GB).
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, fabsf(z), 1.f));
+// The tail of the normal distribution: for a = |z|
+//   1 - Phi(a) = exp(-a^2 / 2) t P(t),  t = 1 / (1 + c a),
+// where t P(t) stands for half the scaled complementary error function.  P is
+// a least-maximum fit on [0, 14], beyond which the exponential is 0 in fp32
+// (Lawson's reweighted least squares on 12,000 points): of relative error
+// 1.5e-7 with eight terms and c = 0.3 (FINE: fp32 results and gradients), of
+// 3.1e-5 with five and c = 0.375 (values that are then rounded to bf16, half a
+// step of which is 3.9e-3).  The tail keeps its relative accuracy, and the
+// exponential, e = exp(-a^2 / 2), is also the density that the derivative
+// needs.  The library's erfcf, which branches by range, took 1.3 ms against
+// 0.9 ms for this in the gradient pass over 2.45M x 256 bf16 (5.0 GB).
+template <bool FINE>
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(FINE ? 0.3f : 0.375f, fabsf(z), 1.f));
     e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);   // exp(-z^2 / 2)
-    float p = 0.0356758525f;
-    p = fmaf(p, t, -0.157207547f);
-    p = fmaf(p, t, 0.206361131f);
-    p = fmaf(p, t, -0.0536906036f);
-    p = fmaf(p, t, 0.128565293f);
-    p = fmaf(p, t, 0.0999123772f);
-    p = fmaf(p, t, 0.120754137f);
-    p = fmaf(p, t, 0.119629287f);
-    const float q = p * t * e;
-    return z < 0.f ? q : 1.f - q;
+    float p;
+    if constexpr (FINE) {
+        p = fmaf(0.0356758525f, t, -0.157207547f);
+        p = fmaf(p, t, 0.206361131f);
+        p = fmaf(p, t, -0.0536906036f);
+        p = fmaf(p, t, 0.128565293f);
+        p = fmaf(p, t, 0.0999123772f);
+        p = fmaf(p, t, 0.120754137f);
+        p = fmaf(p, t, 0.119629287f);
+    } else {
+        p = fmaf(-0.0906485941f, t, 0.200294511f);
+        p = fmaf(p, t, 0.0835541374f);
+        p = fmaf(p, t, 0.157737088f);
+        p = fmaf(p, t, 0.149060699f);
+    }
+    return p * t * e;
 }
 
 __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 
-// act(z) in fp32.  ReLU keeps NaN.
-template <int ACT>
+// act(z) in fp32, for a result of type T.  ReLU keeps NaN.
+template <int ACT, class T>
 __device__ __forceinline__ float act_value(float z, float slope) {
     if constexpr (ACT == SAG_ACT_RELU) return z < 0.f ? 0.f : z;
     else if constexpr (ACT == SAG_ACT_LEAKY_RELU) return z > 0.f ? z : z * slope;
     else if constexpr (ACT == SAG_ACT_GELU) {
+        // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
         float e;
-        return z * normal_cdf(z, e);
+        const float q = normal_tail<sizeof(T) == 4>(z, e);
+        return fmaf(-fabsf(z), q, z < 0.f ? 0.f : z);
     } else if constexpr (ACT == SAG_ACT_SILU) return z * sigmoid(z);
     else return z;
 }
@@ -130,8 +152,8 @@ __device__ __forceinline__ float act_grad(float z, float slope) {
     else if constexpr (ACT == SAG_ACT_LEAKY_RELU) return z > 0.f ? 1.f : slope;
     else if constexpr (ACT == SAG_ACT_GELU) {
         float e;
-        const float c = normal_cdf(z, e);
-        return fmaf(z * 0.39894228040143268f, e, c);             // Phi + z phi
+        const float q = normal_tail<true>(z, e);
+        return fmaf(z * 0.39894228040143268f, e, z < 0.f ? q : 1.f - q);   // Phi + z phi
     } else if constexpr (ACT == SAG_ACT_SILU) {
         const float s = sigmoid(z);
         return s * fmaf(z, 1.f - s, 1.f);

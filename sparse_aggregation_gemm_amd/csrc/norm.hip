@@ -267,7 +267,7 @@ __device__ __forceinline__ void norm_store(T* p, u32x4_t q, const Cols<Vec<T>::N
     float f[V];
     unpack_vec<T>(q, f);
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = act_value<ACT>(fmaf(f[e] - k.mean[k.of(e)], rw[e], k.v[e]), slope);
+    for (int e = 0; e < V; ++e) f[e] = act_value<ACT, T>(fmaf(f[e] - k.mean[k.of(e)], rw[e], k.v[e]), slope);
     store_first<T>(p, f, nc);
 }
 
