@@ -28,8 +28,17 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 // private memory)
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
+// Calls f(std::integral_constant<int, I>) for I in [B, E): register arrays
+// indexed by I stay in registers.
+template <int B, int E, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        static_for<B + 1, E>(f);
+    }
+}
+
 constexpr int kThreads = 256;
-constexpr int kBM = 128;
 constexpr int kRowB = 128;                 // bytes of k per tile row
 constexpr int kStagePitch = 64 * 4 + 16;   // fp32 row of 64 columns, shifted 4 banks a row
 
@@ -85,10 +94,70 @@ struct Eight {
     }
 };
 
+// The derivative of GELU and SiLU at a bf16 argument, from a table in LDS:
+// act'(z) - 1/2 is odd, so the table holds it for the 1664 bf16 values from
+// 2^-8 up to 32, beyond which it is 1/2 in fp32; below 2^-8 it is its slope
+// at 0 times z (to 2e-8).  A lookup is 11 operations and one LDS read against
+// 25 for the formula, and the gradient kernels are bound by their arithmetic:
+// 1.04 and 1.16 ms without it at 2.45M x 256 x 256 (3.8 GB each).  NaN takes
+// the branch of small z and stays NaN.
+constexpr int kTabSize = 1664;
+constexpr uint32_t kTabFirst = 0x3B80u;     // 2^-8
+
+template <int ACT>
+constexpr bool uses_table() { return ACT == SAG_ACT_GELU || ACT == SAG_ACT_SILU; }
+
+template <int ACT>
+__device__ __forceinline__ void build_table(float* tab, int t, int threads) {
+    if constexpr (uses_table<ACT>()) {
+        for (int i = t; i < kTabSize; i += threads)
+            tab[i] = act_grad<ACT>(__uint_as_float((kTabFirst + i) << 16), 0.f) - 0.5f;
+        __syncthreads();
+    }
+}
+
+// act'(z) for the bf16 bits in the high half of `zbits` (the low half is 0).
+template <int ACT>
+__device__ __forceinline__ float table_grad(const float* tab, uint32_t zbits) {
+    const float z = __uint_as_float(zbits);
+    const uint32_t i = ((zbits >> 16) & 0x7fffu) - kTabFirst;
+    const float h = tab[i < kTabSize - 1 ? i : kTabSize - 1];
+    const float near0 = z * (ACT == SAG_ACT_GELU ? 0.79788456080286536f : 0.5f);
+    return 0.5f + (fabsf(z) >= 0x1p-8f ? copysignf(h, z) : near0);
+}
+
+// The eight values of dZ = act'(Z) dropout(G) from the vectors of G and Z.
+template <int ACT, bool DROP>
+__device__ __forceinline__ void dz_of(u32x4_t g, u32x4_t z, const float* tab, const DropArgs& drop, uint32_t node,
+                                      uint32_t block, uint32_t call, float slope, float (&f)[8]) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if constexpr (DROP) drop.draws(node, block, call, w);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        // (two at a time: all eight's temporaries at once cost a wavefront a SIMD)
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = 2 * q; e < 2 * q + 2; ++e) {
+            float x = __uint_as_float(e & 1 ? g[q] & 0xffff0000u : g[q] << 16);
+            if constexpr (DROP) x = drop.apply(x, w, e);
+            const uint32_t zb = e & 1 ? z[q] & 0xffff0000u : z[q] << 16;
+            if constexpr (uses_table<ACT>()) x *= table_grad<ACT>(tab, zb);
+            else if constexpr (ACT != SAG_ACT_NONE) x = times_act_grad<ACT>(x, __uint_as_float(zb), slope);
+            f[e] = x;
+        }
+    }
+}
+
+__device__ __forceinline__ u32x4_t pack8(const float (&f)[8]) {
+    return u32x4_t{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+}
+
 template <class T>
 struct NnArgs {
-    const T* a;
+    const T* a;           // GRAD: G
     int64_t lda, M, K;
+    const T* az;          // GRAD: Z
+    int64_t ldaz;
     const T* bp;          // packed B: [n_blk * BN, Kt]
     int64_t Kt, N;
     int64_t n_blk, m_blk;
@@ -101,29 +170,48 @@ struct NnArgs {
     int64_t ldz;
     T* out;
     int64_t ldo;
+    float out_scale = 1.f;   // of the stored values (a backward product of unscaled dZ)
 };
 
-// WM x WN wavefronts, each MB x NB blocks of 32 x 32.
-template <class T, int BN, int ACT, bool DROP>
-__global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
+template <int BN, bool GRAD>
+constexpr int nn_rows() { return GRAD && BN > 64 ? 64 : 128; }
+
+// WM x WN wavefronts, each MB x NB blocks of 32 x 32.  GRAD (bf16, 256
+// columns): A is dZ, computed from G and Z on its way into LDS and stored
+// nowhere, once per row as long as the columns make one block; the epilogue
+// only stores.
+template <class T, int BN, int ACT, bool DROP, bool GRAD>
+__global__ __launch_bounds__((BN == 256 ? 512 : 256), GRAD ? (BN == 256 ? 4 : 3) : 1) void dense_nn(NnArgs<T> p) {
+    constexpr int kThreads = BN == 256 ? 512 : 256, kBM = nn_rows<BN, GRAD>();
     constexpr int V = Vec<T>::N;
     constexpr int CK = kRowB / static_cast<int>(sizeof(T));
-    constexpr int WN = BN == 128 ? 2 : 1, WM = 4 / WN;
+    constexpr int WN = BN >= 128 ? BN / 64 : 1, WM = kThreads / 64 / WN;
     constexpr int MB = kBM / WM / 32, NB = BN / WN / 32;
     constexpr int UA = kBM * 8 / kThreads, UB = BN * 8 / kThreads;   // 16-byte units per thread
     constexpr int kTiles = (kBM + BN) * kRowB;
-    constexpr int kStage = 4 * 32 * kStagePitch;
+    constexpr int kStage = kThreads / 64 * 32 * kStagePitch;
     __shared__ __attribute__((aligned(16))) unsigned char lds[kTiles > kStage ? kTiles : kStage];
     unsigned char* As = lds;
     unsigned char* Bs = lds + kBM * kRowB;
 
+    __shared__ float tab[GRAD && uses_table<ACT>() ? kTabSize : 1];
+    if constexpr (GRAD) build_table<ACT>(tab, threadIdx.x, kThreads);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wm = wave / WN, wn = wave % WN;
     const int h = lane >> 5, l32 = lane & 31;
     const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
     const int64_t m0 = tile / p.n_blk * kBM, n0 = tile % p.n_blk * BN;
 
-    u32x4_t ra[UA], rb[UB];
+    u32x4_t ra[UA], rz[GRAD ? UA : 1], rb[UB];
+    uint32_t node[GRAD && DROP ? UA : 1], call = 0;
+    if constexpr (DROP) call = p.drop.call_now();
+    if constexpr (GRAD && DROP) {
+#pragma unroll
+        for (int i = 0; i < UA; ++i) {
+            const int64_t row = m0 + (t + i * kThreads) / 8;
+            node[i] = p.drop.node_of(row < p.M ? row : p.M - 1);
+        }
+    }
     const int64_t last = (p.K + V - 1) / V * V - V;
     auto load = [&](int64_t k0) {
 #pragma unroll
@@ -132,6 +220,7 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
             const int64_t row = m0 + r < p.M ? m0 + r : p.M - 1;
             const int64_t k = k0 + u * V;
             ra[i] = load16(p.a + row * p.lda + (k < last ? k : last));
+            if constexpr (GRAD && ACT != SAG_ACT_NONE) rz[i] = load16(p.az + row * p.ldaz + (k < last ? k : last));
         }
 #pragma unroll
         for (int i = 0; i < UB; ++i) {
@@ -145,6 +234,12 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
         for (int i = 0; i < UA; ++i) {
             const int q = t + i * kThreads, r = q >> 3, u = q & 7;
             const int64_t left = p.K - k0 - u * V;
+            if constexpr (GRAD) {
+                float f[8];
+                dz_of<ACT, DROP>(ra[i], rz[ACT == SAG_ACT_NONE ? 0 : i], tab, p.drop, node[DROP ? i : 0],
+                                 static_cast<uint32_t>((k0 >> 3) + u), call, p.slope, f);
+                ra[i] = pack8(f);
+            }
             store16(As + r * kRowB + ((u ^ swz(r)) << 4),
                     edge ? keep_first<T>(ra[i], left < V ? (left > 0 ? static_cast<int>(left) : 0) : V) : ra[i]);
         }
@@ -211,8 +306,6 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
     float bias[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) bias[e] = p.bias && e < live ? p.bias[col + e] : 0.f;
-    uint32_t call = 0;
-    if constexpr (DROP) call = p.drop.call_now();
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
         const int64_t row0 = m0 + (wm * MB + i) * 32;
@@ -229,22 +322,24 @@ __global__ __launch_bounds__(kThreads) void dense_nn(NnArgs<T> p) {
             const int64_t row = row0 + r;
             if (row >= p.M || live <= 0) continue;
             Eight<T> rv;
-            if (p.res) rv.load(p.res + row * p.ldr + col, live);
+            if (!GRAD && p.res) rv.load(p.res + row * p.ldr + col, live);
             const float4 lo = *reinterpret_cast<const float4*>(st + r * kStagePitch + u * 32);
             const float4 hi = *reinterpret_cast<const float4*>(st + r * kStagePitch + u * 32 + 16);
             float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] += bias[e];
-            if (p.z) Eight<T>::put(p.z + row * p.ldz + col, y, live);
+            if (!GRAD && p.z) Eight<T>::put(p.z + row * p.ldz + col, y, live);
+            if constexpr (!GRAD) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = act_value<ACT, T>(y[e], p.slope);
-            if constexpr (DROP) {
+                for (int e = 0; e < 8; ++e) y[e] = ACT == SAG_ACT_NONE && !DROP ? y[e] * p.out_scale : act_value<ACT, T>(y[e], p.slope);
+            }
+            if constexpr (DROP && !GRAD) {
                 uint32_t dw[4];
                 p.drop.draws(p.drop.node_of(row), static_cast<uint32_t>(col >> 3), call, dw);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = p.drop.apply(y[e], dw, e);
             }
-            if (p.res) {
+            if (!GRAD && p.res) {
                 float f[8];
                 rv.get(f);
 #pragma unroll
@@ -293,7 +388,7 @@ __global__ __launch_bounds__(kThreads) void dense_dz(int64_t M, int64_t N, int64
         float zf[8];
         zv.get(zf);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= act_grad<ACT>(zf[e], slope);
+        for (int e = 0; e < 8; ++e) f[e] = times_act_grad<ACT>(f[e], zf[e], slope);
     }
     Eight<T>::put(hi + row * ldh + col, f, live);
     if (lo) {
@@ -304,41 +399,273 @@ __global__ __launch_bounds__(kThreads) void dense_dz(int64_t M, int64_t N, int64
     }
 }
 
-__global__ void add_in_place(float* __restrict__ c, const float* __restrict__ d, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i < n) c[i] += d[i];
+// ---- dW (bf16) ---------------------------------------------------------------------------
+// C[K, N] = X^T dZ: a workgroup takes 256 rows of C (columns of X) by 128
+// columns and a run of rows of X, 32 rows a step through LDS (two stages, one
+// barrier a step; the next step's loads in registers), and leaves its
+// fp32 sums as a partial; dense_tn_reduce adds the partials in order.  The
+// matrix cores reduce over rows, so both operands come out of the row-major
+// tiles by the LDS transpose read ds_read_b64_tr_b16 (for four rows and
+// sixteen columns lane i of sixteen gets column i of the four rows).
+// A bf16 dZ alone would put 2^-9 into every term of an fp32 result, so dZ is
+// held as hi + lo (LO), both bf16, and multiplied twice; without an activation
+// or with ReLU, dZ is G or 0 exactly, up to the dropout scale, which the
+// reduction applies.  FROM_G: dZ comes from G and Z (z); otherwise hi and lo
+// are read.  Column sums (db) are taken of the fp32 dZ on its way into LDS.
+constexpr int kTnWaves = 16, kTnThreads = kTnWaves * 64, kTnK = 256, kTnN = 128, kTnRows = 64;
+constexpr int kTnPX = kTnK * 2 + 64, kTnPZ = kTnN * 2 + 64;     // row pitches in LDS: 16 banks a row apart
+
+struct TnArgs {
+    const uint16_t* x;
+    int64_t ldx, M, K, N;
+    const uint16_t* g;          // FROM_G: G, else hi
+    int64_t ldg;
+    const uint16_t* z;          // FROM_G: Z, else lo
+    int64_t ldz;
+    float slope;
+    DropArgs drop;
+    int64_t n_kblk, n_nblk, rows_per_chunk;
+    float* part;                // [chunk][n_kblk * 256][n_nblk * 128]
+    float* part_cs;             // [chunk][n_nblk * 128], nullable
+};
+
+template <int ACT>
+constexpr bool dz_exact() { return ACT == SAG_ACT_NONE || ACT == SAG_ACT_RELU; }
+
+template <int ACT, bool DROP, bool LO, bool FROM_G>
+__global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
+    typedef short i16x4_t __attribute__((ext_vector_type(4)));
+    constexpr int SX = kTnRows * kTnPX, SZ = kTnRows * kTnPZ;
+    constexpr int STAGE = SX + (LO ? 2 : 1) * SZ;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    float* tab = reinterpret_cast<float*>(lds + 2 * STAGE);
+    if constexpr (FROM_G) build_table<ACT>(tab, threadIdx.x, kTnThreads);
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int wk = wave >> 2, wn = wave & 3;
+    // the blocks of one chunk next to each other on one XCD
+    const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int64_t nb = tile % p.n_nblk, kb = tile / p.n_nblk % p.n_kblk, chunk = tile / (p.n_nblk * p.n_kblk);
+    const int64_t k0 = kb * kTnK, n0 = nb * kTnN;
+    const int64_t m_begin = chunk * p.rows_per_chunk;
+    const int64_t m_end = m_begin + p.rows_per_chunk < p.M ? m_begin + p.rows_per_chunk : p.M;
+
+    // this thread's units: two of X (rows t / 32 and 32 more), one of dZ
+    const int xr = t >> 5, xc = (t & 31) * 8, zr = t >> 4, zc = (t & 15) * 8;
+    const int64_t xlast = (p.K + 7) / 8 * 8 - 8, zlast = (p.N + 7) / 8 * 8 - 8;
+    const int64_t xcol = k0 + xc < xlast ? k0 + xc : xlast, zcol = n0 + zc < zlast ? n0 + zc : zlast;
+    const uint32_t block = static_cast<uint32_t>((n0 + zc) >> 3);
+    uint32_t call = 0;
+    if constexpr (DROP && FROM_G) call = p.drop.call_now();
+    u32x4_t rx[2], rg, rz;
+    uint32_t node = 0;
+    // the rows of the step that is loaded next; a row past the chunk is read
+    // from the operand's first, and not used
+    const char* px = reinterpret_cast<const char*>(p.x + (m_begin + xr) * p.ldx + xcol);
+    const char* pg = reinterpret_cast<const char*>(p.g + (m_begin + zr) * p.ldg + zcol);
+    const char* pz = reinterpret_cast<const char*>(p.z + (m_begin + zr) * p.ldz + zcol);
+    const int64_t half_x = 64 * p.ldx, step_g = 128 * p.ldg, step_z = 128 * p.ldz;   // bytes: 32 rows, 64 rows
+    constexpr bool kReadZ = FROM_G ? ACT != SAG_ACT_NONE : LO;
+    auto load = [&](int64_t m) __attribute__((always_inline)) {
+        rx[0] = load16(m + xr < m_end ? px : reinterpret_cast<const char*>(p.x));
+        rx[1] = load16(m + xr + 32 < m_end ? px + half_x : reinterpret_cast<const char*>(p.x));
+        px += 2 * half_x;
+        const bool in = m + zr < m_end;
+        rg = load16(in ? pg : reinterpret_cast<const char*>(p.g));
+        pg += step_g;
+        if constexpr (kReadZ) {
+            rz = load16(in ? pz : reinterpret_cast<const char*>(p.z));
+            pz += step_z;
+        }
+        if constexpr (DROP && FROM_G) node = p.drop.node_of(in ? m + zr : m_begin);
+    };
+    float cs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = 0.f;
+    // (rows past the chunk are written as zeros, in both operands: a clamped
+    // row of X may hold infinities)
+    auto store = [&](int st, int64_t m) __attribute__((always_inline)) {
+        unsigned char* Xs = lds + st * STAGE;
+        unsigned char* Hs = Xs + SX;
+        const u32x4_t none = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            store16(Xs + (xr + 32 * i) * kTnPX + xc * 2, m + xr + 32 * i < m_end ? rx[i] : none);
+        const bool in = m + zr < m_end;
+        if constexpr (FROM_G) {
+            float f[8];
+            dz_of<ACT, DROP>(rg, rz, tab, p.drop, node, block, call, p.slope, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[e] = in ? f[e] : 0.f;
+                cs[e] += f[e];
+            }
+            const u32x4_t hi = pack8(f);
+            store16(Hs + zr * kTnPZ + zc * 2, hi);
+            if constexpr (LO) {
+                float hf[8];
+                unpack<uint16_t>(as_uint4(hi), hf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] -= hf[e];
+                store16(Hs + SZ + zr * kTnPZ + zc * 2, pack8(f));
+            }
+        } else {
+            const u32x4_t hi = in ? rg : none, lo = LO && in ? rz : none;
+            float f[8];
+            unpack<uint16_t>(as_uint4(hi), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) cs[e] += f[e];
+            store16(Hs + zr * kTnPZ + zc * 2, hi);
+            if constexpr (LO) {
+                unpack<uint16_t>(as_uint4(lo), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) cs[e] += f[e];
+                store16(Hs + SZ + zr * kTnPZ + zc * 2, lo);
+            }
+        }
+    };
+    f32x16_t acc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    const int g4 = lane >> 4, q4 = (lane & 15) >> 2, r4 = lane & 3;
+    auto frag = [&](const unsigned char* base, int pitch) __attribute__((always_inline)) {
+        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(base));
+        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(base + 4 * pitch));
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto multiply = [&](int st) __attribute__((always_inline)) {
+        const unsigned char* Xs = lds + st * STAGE;
+        const unsigned char* Hs = Xs + SX;
+#pragma unroll
+        for (int s = 0; s < kTnRows / 16; ++s) {           // 16 rows per product
+            const int m = 16 * s + 8 * (g4 >> 1) + q4, c = 16 * (g4 & 1) + 4 * r4;
+            bf16x8_t xa[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) xa[i] = frag(Xs + m * kTnPX + (wk * 64 + 32 * i + c) * 2, kTnPX);
+            const unsigned char* h = Hs + m * kTnPZ + (wn * 32 + c) * 2;
+            if constexpr (LO) {
+                const bf16x8_t yl = frag(h + SZ, kTnPZ);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], yl, acc[i], 0, 0, 0);
+            }
+            const bf16x8_t yb = frag(h, kTnPZ);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], yb, acc[i], 0, 0, 0);
+        }
+    };
+    const int64_t steps = (m_end - m_begin + kTnRows - 1) / kTnRows;
+    load(m_begin);
+    store(0, m_begin);
+    load(m_begin + kTnRows);
+    __syncthreads();
+    // step s: stage s + 1, load s + 2, multiply s (past the chunk zeros are staged)
+    for (int64_t s = 0; s < steps; ++s) {
+        const int cur = static_cast<int>(s & 1);
+        store(cur ^ 1, m_begin + (s + 1) * kTnRows);
+        load(m_begin + (s + 2) * kTnRows);
+        multiply(cur);
+        __syncthreads();
+    }
+    const int64_t pn = p.n_nblk * kTnN;
+    float* out = p.part + (chunk * p.n_kblk * kTnK + k0 + wk * 64 + 4 * (lane / 32)) * pn + n0 + wn * 32 + lane % 32;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            *out = acc[i][r];
+            out += r % 4 == 3 ? 5 * pn : pn;
+        }
+    if (p.part_cs && kb == 0) {
+        // the row threads of each column, in order
+        float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) red[zr * kTnN + zc + e] = cs[e];
+        __syncthreads();
+        if (t < kTnN) {
+            float sum = 0.f;
+            for (int r = 0; r < kTnRows; ++r) sum += red[r * kTnN + t];
+            p.part_cs[chunk * pn + n0 + t] = sum;
+        }
+    }
+}
+
+// dW and db: the partials in chunk order, four threads to an element, each a
+// quarter of the chunks, eight loads ahead; times the dropout scale where the
+// sums are of G itself.
+__global__ __launch_bounds__(256) void dense_tn_reduce(const float* __restrict__ part, const float* __restrict__ part_cs,
+                                                       int64_t chunks, int64_t K, int64_t N, int64_t pk, int64_t pn,
+                                                       float scale, float* __restrict__ dW, float* __restrict__ db) {
+    __shared__ float sh[256];
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+    const int quarter = threadIdx.x >> 6;
+    const int64_t total = (dW ? K * N : 0) + (db ? N : 0);
+    const float* src = part;
+    int64_t stride = pk * pn;
+    float* dst = nullptr;
+    if (idx < total) {
+        if (dW && idx < K * N) {
+            src = part + idx / N * pn + idx % N;
+            dst = dW + idx;
+        } else {
+            const int64_t n = idx - (dW ? K * N : 0);
+            src = part_cs + n;
+            stride = pn;
+            dst = db + n;
+        }
+    }
+    const int64_t per = (chunks + 3) / 4, lo = quarter * per, hi = lo + per < chunks ? lo + per : chunks;
+    float s = 0.f;
+    if (dst) {
+        int64_t c = lo;
+        for (; c + 8 <= hi; c += 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = src[(c + u) * stride];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
+        for (; c < hi; ++c) s += src[c * stride];
+    }
+    sh[threadIdx.x] = s;
+    __syncthreads();
+    if (quarter == 0 && dst) *dst = (((sh[threadIdx.x] + sh[threadIdx.x + 64]) + sh[threadIdx.x + 128]) + sh[threadIdx.x + 192]) * scale;
 }
 
 int64_t k_pad(int64_t K, sag_dtype dt) { return round_up(K, kRowB / elt_size(dt)); }
 size_t pack_bytes(int64_t K, int64_t N, sag_dtype dt) {
-    return static_cast<size_t>(round_up(N, 128) * k_pad(K, dt) * elt_size(dt));
+    return static_cast<size_t>(round_up(N, 256) * k_pad(K, dt) * elt_size(dt));
 }
 
 // Packs B ([K, N]; element (k, n) at b[k sk + n sn]) and multiplies.
-template <class T>
+template <class T, bool GRAD = false>
 sag_status nn_run(const char* what, sag_act act, NnArgs<T> p, const T* b, int64_t sk, int64_t sn, T* bp, sag_dtype dt,
                   hipStream_t s) {
-    const int BN = p.N <= 64 ? 64 : 128;
+    const int BN = GRAD && p.N > 128 ? 256 : (p.N <= 64 ? 64 : 128);
     p.Kt = k_pad(p.K, dt);
     p.bp = bp;
     p.n_blk = cdiv(p.N, BN);
-    p.m_blk = cdiv(p.M, kBM);
-    if (p.n_blk * p.m_blk >= (1 << 24)) return fail(SAG_E_UNSUPPORTED, std::string(what) + ": too many tiles for one launch");
+    p.m_blk = cdiv(p.M, GRAD && BN > 64 ? 64 : 128);
+    if (p.n_blk * p.m_blk >= (1 << 23)) return fail(SAG_E_UNSUPPORTED, std::string(what) + ": too many tiles for one launch");
     const int64_t total = p.n_blk * BN * p.Kt;
     dense_pack<T><<<dim3(static_cast<unsigned>(cdiv(total, 256))), 256, 0, s>>>(b, sk, sn, p.K, p.N, p.Kt, total, bp);
     SAG_LAUNCH_CHECK();
+    const int64_t rows = p.M * p.K * (p.az ? 2 : 1) + p.M * p.N * (1 + (p.z ? 1 : 0) + (p.res ? 1 : 0));
     TraceScope trace(trace_enabled() ? shape_name(what, dt == SAG_BF16 ? "bf16" : "f32", p.M, p.K, p.N) : std::string(),
-                     s, elt_size(dt) * (p.M * p.K + p.K * p.N + p.M * p.N * (1 + (p.z ? 1 : 0) + (p.res ? 1 : 0))),
-                     2 * p.M * p.K * p.N);
+                     s, elt_size(dt) * (rows + p.K * p.N), 2 * p.M * p.K * p.N);
     const dim3 grid(static_cast<unsigned>(p.n_blk * p.m_blk));
     with_act(act, [&](auto ac) {
         constexpr int ACT = decltype(ac)::value;
-        if (BN == 64) {
-            if (p.drop.T) dense_nn<T, 64, ACT, true><<<grid, kThreads, 0, s>>>(p);
-            else dense_nn<T, 64, ACT, false><<<grid, kThreads, 0, s>>>(p);
-        } else {
-            if (p.drop.T) dense_nn<T, 128, ACT, true><<<grid, kThreads, 0, s>>>(p);
-            else dense_nn<T, 128, ACT, false><<<grid, kThreads, 0, s>>>(p);
+        auto go = [&](auto bn) {
+            constexpr int BN = decltype(bn)::value;
+            constexpr int NT = BN == 256 ? 512 : 256;
+            if (p.drop.T) dense_nn<T, BN, ACT, true, GRAD><<<grid, NT, 0, s>>>(p);
+            else dense_nn<T, BN, ACT, false, GRAD><<<grid, NT, 0, s>>>(p);
+        };
+        if (BN == 64) go(std::integral_constant<int, 64>{});
+        else if (BN == 128) go(std::integral_constant<int, 128>{});
+        if constexpr (GRAD) {
+            if (BN == 256) go(std::integral_constant<int, 256>{});
         }
     });
     SAG_LAUNCH_CHECK();
@@ -350,11 +677,37 @@ sag_status forward_typed(NnArgs<T> p, const void* W, sag_act act, sag_dtype dt, 
     return nn_run<T>("dense", act, p, static_cast<const T*>(W), p.N, 1, static_cast<T*>(ws), dt, s);
 }
 
+// ---- backward ------------------------------------------------------------------------------
+// bf16 layers of up to 256 inputs never store dZ: the input gradient and the
+// weight gradient each compute it from G and Z on its way into LDS (once a
+// row, as 256 columns make one block in both).  Wider ones would compute it
+// once a block of 256, where it costs more than the products (45 operations
+// an element against 0.25 matrix operations' time a column block), so there it
+// is stored first, as hi (and lo, where it is not exact); fp32, bound by the
+// matrix cores, stores it as well.
+bool dz_from_g(int64_t K, sag_dtype dt) { return dt == SAG_BF16 && K <= 256; }
+
+struct TnPlan {
+    int64_t n_kblk, n_nblk, chunks, rows_per_chunk;
+};
+
+// One workgroup of sixteen wavefronts a CU, of at least 128 rows.
+TnPlan tn_plan(int64_t M, int64_t K, int64_t N) {
+    TnPlan p;
+    p.n_kblk = cdiv(K, kTnK);
+    p.n_nblk = cdiv(N, kTnN);
+    int64_t want = cdiv(256, p.n_kblk * p.n_nblk);
+    const int64_t most = cdiv(M > 0 ? M : 1, 2 * kTnRows);
+    if (want > most) want = most;
+    p.rows_per_chunk = round_up(cdiv(M > 0 ? M : 1, want), kTnRows);
+    p.chunks = cdiv(M, p.rows_per_chunk);
+    return p;
+}
+
 struct BwdWs {
     void *bp, *hi, *lo, *tn;
-    float *c2, *cs2;
-    size_t tn_bytes;
-    size_t used;
+    float *part, *part_cs;
+    size_t tn_bytes, used;
     bool fits;
 };
 
@@ -362,17 +715,67 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, sag_dtype dt, void* ws, size_t byt
     Carver c(ws, bytes);
     BwdWs w{};
     w.bp = c.take<char>(pack_bytes(N, K, dt));
-    w.hi = c.take<char>(dense_bytes(M, N, dt));
+    if (!dz_from_g(K, dt)) w.hi = c.take<char>(dense_bytes(M, N, dt));
     if (dt == SAG_BF16) {
-        w.lo = c.take<char>(dense_bytes(M, N, dt));
-        w.c2 = c.take<float>(K * N + N);
-        w.cs2 = w.c2 ? w.c2 + K * N : nullptr;
+        if (!dz_from_g(K, dt)) w.lo = c.take<char>(dense_bytes(M, N, dt));
+        const TnPlan p = tn_plan(M, K, N);
+        w.part = c.take<float>(p.chunks * p.n_kblk * kTnK * p.n_nblk * kTnN);
+        w.part_cs = c.take<float>(p.chunks * p.n_nblk * kTnN);
+    } else {
+        w.tn_bytes = gemm_tn_ws_bytes(M, round_up(K, vec_elems(dt)), N, dt);
+        w.tn = c.take<char>(w.tn_bytes);
+        w.part = c.take<float>(K * N);   // dW when only db is wanted
     }
-    w.tn_bytes = gemm_tn_ws_bytes(M, round_up(K, vec_elems(dt)), N, dt);
-    w.tn = c.take<char>(w.tn_bytes);
     w.used = c.used();
     w.fits = c.fits();
     return w;
+}
+
+template <int ACT, bool DROP, bool LO, bool FROM_G>
+sag_status launch_tn(const TnArgs& a, int64_t chunks, hipStream_t s) {
+    constexpr int lds = 2 * (kTnRows * kTnPX + (LO ? 2 : 1) * kTnRows * kTnPZ) +
+                        (FROM_G && uses_table<ACT>() ? kTabSize * 4 : 0);
+    static_assert(lds >= kTnRows * kTnN * 4, "column-sum buffer");
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_tn<ACT, DROP, LO, FROM_G>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    SAG_CHECK_HIP(attr);
+    const unsigned grid = static_cast<unsigned>(chunks * a.n_kblk * a.n_nblk);
+    dense_tn<ACT, DROP, LO, FROM_G><<<grid, kTnThreads, lds, s>>>(a);
+    SAG_LAUNCH_CHECK();
+    return SAG_OK;
+}
+
+// bf16: dW and db from G and Z, or from stored hi and lo.
+sag_status tn_run(sag_act act, TnArgs a, bool from_g, float* dW, float* db, const BwdWs& w, hipStream_t s) {
+    const TnPlan p = tn_plan(a.M, a.K, a.N);
+    a.n_kblk = p.n_kblk; a.n_nblk = p.n_nblk; a.rows_per_chunk = p.rows_per_chunk;
+    a.part = w.part; a.part_cs = db ? w.part_cs : nullptr;
+    const bool exact = act == SAG_ACT_NONE || act == SAG_ACT_RELU;
+    // a sum over G itself is scaled once, at the end
+    const float scale = exact && a.drop.T ? a.drop.scale : 1.f;
+    if (exact) a.drop.scale = 1.f;
+    TraceScope trace(trace_enabled() ? shape_name("dense_dw", "bf16", a.M, a.K, a.N) : std::string(), s,
+                     2 * (a.M * a.K + a.M * a.N * (act == SAG_ACT_NONE || (exact && !from_g) ? 1 : 2)) + 4 * (a.K * a.N + a.N),
+                     (exact ? 2 : 4) * a.M * a.K * a.N);
+    if (p.chunks) {
+        sag_status st = SAG_OK;
+        if (!from_g) {
+            st = exact ? launch_tn<SAG_ACT_NONE, false, false, false>(a, p.chunks, s)
+                       : launch_tn<SAG_ACT_NONE, false, true, false>(a, p.chunks, s);
+        } else {
+            with_act(act, [&](auto ac) {
+                constexpr int ACT = decltype(ac)::value;
+                st = a.drop.T ? launch_tn<ACT, true, !dz_exact<ACT>(), true>(a, p.chunks, s)
+                              : launch_tn<ACT, false, !dz_exact<ACT>(), true>(a, p.chunks, s);
+            });
+        }
+        SAG_TRY(st);
+    }
+    const int64_t total = (dW ? a.K * a.N : 0) + (db ? a.N : 0);
+    dense_tn_reduce<<<dim3(static_cast<unsigned>(cdiv(total, 64))), 256, 0, s>>>(
+        w.part, w.part_cs, p.chunks, a.K, a.N, p.n_kblk * kTnK, p.n_nblk * kTnN, scale, dW, db);
+    SAG_LAUNCH_CHECK();
+    return SAG_OK;
 }
 
 template <class T>
@@ -380,39 +783,51 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
                           const DropArgs& drop, const T* Z, int64_t ldz, const T* G, int64_t ldg, float* dW, float* db,
                           T* dX, int64_t ldd, sag_dtype dt, const BwdWs& w, hipStream_t s) {
     const int64_t ldh = ldv(N, dt), upr = cdiv(N, 8);
+    const bool from_g = dz_from_g(K, dt), exact = act == SAG_ACT_NONE || act == SAG_ACT_RELU;
     T* hi = static_cast<T*>(w.hi);
-    T* lo = static_cast<T*>(w.lo);
-    if (M > 0) {
+    T* lo = exact ? nullptr : static_cast<T*>(w.lo);
+    if (M > 0 && !from_g) {
         const int64_t blocks = cdiv(M * upr, kThreads);
         if (blocks >= (1 << 24)) return fail(SAG_E_UNSUPPORTED, "dense backward: too many elements for one launch");
         TraceScope trace(trace_enabled() ? shape_name("dense_dz", dt == SAG_BF16 ? "bf16" : "f32", M, N, 0) : std::string(),
                          s, elt_size(dt) * M * N * (2 + (act != SAG_ACT_NONE ? 1 : 0) + (lo ? 1 : 0)), 0);
+        // (exact in bf16: G or 0, the products take the dropout scale)
+        DropArgs unscaled = drop;
+        if (exact && dt == SAG_BF16) unscaled.scale = 1.f;
         with_act(act, [&](auto ac) {
             dense_dz<T, decltype(ac)::value><<<dim3(static_cast<unsigned>(blocks)), kThreads, 0, s>>>(
-                M, N, upr, Z, ldz, G, ldg, slope, drop, hi, lo, ldh);
+                M, N, upr, Z, ldz, G, ldg, slope, unscaled, hi, lo, ldh);
         });
         SAG_LAUNCH_CHECK();
     }
     if (dX && M > 0) {
         NnArgs<T> p{};
-        p.a = hi; p.lda = ldh; p.M = M; p.K = N; p.N = K;
-        p.drop = DropArgs{};
+        p.M = M; p.K = N; p.N = K;
         p.out = dX; p.ldo = ldd;
-        SAG_TRY(nn_run<T>("dense_dx", SAG_ACT_NONE, p, W, 1, N, static_cast<T*>(w.bp), dt, s));
-    }
-    if (dW || db) {
-        GemmA a;
-        a.a1 = X; a.lda1 = ldx; a.k1 = K; a.m1 = M;
-        float* cw = dW ? dW : w.c2;
-        SAG_TRY(gemm_tn_run(M, N, a, hi, ldh, nullptr, 0, cw, N, db, dt, w.tn, w.tn_bytes, s));
-        if (lo) {
-            SAG_TRY(gemm_tn_run(M, N, a, lo, ldh, nullptr, 0, w.c2, N, db ? w.cs2 : nullptr, dt, w.tn, w.tn_bytes, s));
-            if (dW) add_in_place<<<dim3(static_cast<unsigned>(cdiv(K * N, 256))), 256, 0, s>>>(dW, w.c2, K * N);
-            if (db) add_in_place<<<dim3(static_cast<unsigned>(cdiv(N, 256))), 256, 0, s>>>(db, w.cs2, N);
-            SAG_LAUNCH_CHECK();
+        if (from_g) {
+            if constexpr (sizeof(T) == 2) {
+                p.a = G; p.lda = ldg; p.az = act == SAG_ACT_NONE ? nullptr : Z; p.ldaz = ldz;
+                p.slope = slope; p.drop = drop;
+                SAG_TRY((nn_run<T, true>("dense_dx", act, p, W, 1, N, static_cast<T*>(w.bp), dt, s)));
+            }
+        } else {
+            p.a = hi; p.lda = ldh;
+            p.out_scale = exact && dt == SAG_BF16 && drop.T ? drop.scale : 1.f;
+            SAG_TRY(nn_run<T>("dense_dx", SAG_ACT_NONE, p, W, 1, N, static_cast<T*>(w.bp), dt, s));
         }
     }
-    return SAG_OK;
+    if (!dW && !db) return SAG_OK;
+    if constexpr (sizeof(T) == 2) {
+        TnArgs a{};
+        a.x = X; a.ldx = ldx; a.M = M; a.K = K; a.N = N; a.slope = slope; a.drop = drop;
+        a.g = from_g ? G : hi; a.ldg = from_g ? ldg : ldh;
+        a.z = from_g ? Z : lo; a.ldz = from_g ? ldz : ldh;
+        return tn_run(act, a, from_g, dW, db, w, s);
+    } else {
+        GemmA a;
+        a.a1 = X; a.lda1 = ldx; a.k1 = K; a.m1 = M;
+        return gemm_tn_run(M, N, a, hi, ldh, nullptr, 0, dW ? dW : w.part, N, db, dt, w.tn, w.tn_bytes, s);
+    }
 }
 
 sag_status check_sizes(const char* who, int64_t M, int64_t K, int64_t N, sag_act act, float slope, sag_dtype dt) {

@@ -160,6 +160,13 @@ __device__ __forceinline__ float act_grad(float z, float slope) {
     } else return 1.f;
 }
 
+// g act'(z); where ReLU is off the result is 0 whatever g is.
+template <int ACT>
+__device__ __forceinline__ float times_act_grad(float g, float z, float slope) {
+    if constexpr (ACT == SAG_ACT_RELU) return z > 0.f ? g : 0.f;
+    else return g * act_grad<ACT>(z, slope);
+}
+
 // f(std::integral_constant<int, act>) for a runtime activation.
 template <class F>
 auto with_act(sag_act a, F&& f) {

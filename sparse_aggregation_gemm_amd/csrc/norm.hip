@@ -500,7 +500,7 @@ __device__ __forceinline__ float grad_a(float x, float g, float mean, float rstd
         const float dl = (x - (dh - b)) - (mean + b);
         z += fmaf(dh, k.rl, dl * k.rh);
     }
-    return act_grad<ACT>(z, slope) * g;
+    return times_act_grad<ACT>(g, z, slope);
 }
 
 // dX of one vector from the means m0 of h and m1 of h xhat.
