@@ -351,6 +351,169 @@ __global__ __launch_bounds__((BN == 256 ? 512 : 256), GRAD ? (BN == 256 ? 4 : 3)
     }
 }
 
+// ---- few tiles ---------------------------------------------------------------------------
+// The same product where 32 x 32 tiles do not fill the chip: a workgroup of
+// up to sixteen wavefronts does one tile, each wavefront every sixteenth
+// 128-byte piece of k, and their sums are added in LDS in a fixed tree before
+// the epilogue.  Operands go from memory straight into the matrix cores'
+// registers, B from the weight as it lies (two bytes or four a load for the
+// forward product, whole vectors along the rows for the gradient's), so there
+// is one launch, no workspace and one round of loads in front of the products.
+// What bounds it is latency: launch, one memory round trip and the tree.
+constexpr int kFewPitch = 36;              // floats of a tile row in LDS
+constexpr int kFewTiles = 512;             // taken up to two workgroups a CU
+
+// Sixteen bytes from an address aligned to an element.
+template <class T>
+__device__ __forceinline__ u32x4_t load16_any(const T* p) {
+    struct __attribute__((packed, aligned(sizeof(T)))) Any { u32x4_t v; };
+    return reinterpret_cast<const Any*>(p)->v;
+}
+
+template <class T, int ACT, bool DROP, bool GRAD>
+__global__ __launch_bounds__(1024) void dense_few(NnArgs<T> p, const T* __restrict__ w, int64_t ldw) {
+    constexpr int V = Vec<T>::N;
+    constexpr int CK = kRowB / static_cast<int>(sizeof(T));
+    extern __shared__ __attribute__((aligned(16))) float part[];   // [wavefront][32][kFewPitch]
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = blockDim.x >> 6;
+    const int h = lane >> 5, l32 = lane & 31;
+    const uint32_t tm = blockIdx.x / static_cast<uint32_t>(p.n_blk), tn = blockIdx.x % static_cast<uint32_t>(p.n_blk);
+    const int64_t m0 = static_cast<int64_t>(tm) * 32, n0 = static_cast<int64_t>(tn) * 32;
+    const int64_t row = m0 + l32 < p.M ? m0 + l32 : p.M - 1, col = n0 + l32 < p.N ? n0 + l32 : p.N - 1;
+    uint32_t call = 0, node = 0;
+    if constexpr (DROP) call = p.drop.call_now();
+    if constexpr (DROP && GRAD) node = p.drop.node_of(row);
+    const T* ar = p.a + row * p.lda;
+    const T* zr = GRAD && ACT != SAG_ACT_NONE ? p.az + row * p.ldaz : nullptr;
+    f32x16_t acc;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+    for (int64_t k0 = static_cast<int64_t>(wave) * CK; k0 < p.K; k0 += static_cast<int64_t>(waves) * CK) {
+        u32x4_t a[4], z[4], b[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            // this lane's V values of k, the last piece's padded with zeros
+            const int64_t k = k0 + s * (CK / 4) + h * V;
+            const int left = p.K - k >= V ? V : (p.K > k ? static_cast<int>(p.K - k) : 0);
+            const int64_t ka = left ? k : 0;
+            a[s] = load16(ar + ka);
+            if constexpr (GRAD && ACT != SAG_ACT_NONE) z[s] = load16(zr + ka);
+            if constexpr (GRAD) {
+                // W's row `col` along k
+                const T* wr = w + col * ldw + ka;
+                if (left == V) {
+                    b[s] = load16_any(wr);
+                } else {
+                    b[s] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        uint32_t x = 0u;
+                        if (e < left) {
+                            if constexpr (sizeof(T) == 2) x = static_cast<uint32_t>(wr[e]) << (16 * (e & 1));
+                            else x = __float_as_uint(wr[e]);
+                        }
+                        b[s][e * static_cast<int>(sizeof(T)) / 4] |= x;
+                    }
+                }
+            } else {
+                // V rows of W at column `col`
+                b[s] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const T x = w[(e < left ? k + e : 0) * ldw + col];
+                    if constexpr (sizeof(T) == 2) b[s][e / 2] |= (e < left ? static_cast<uint32_t>(x) : 0u) << (16 * (e & 1));
+                    else b[s][e] = e < left ? __float_as_uint(x) : 0u;
+                }
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int64_t k = k0 + s * (CK / 4) + h * V;
+            const int left = p.K - k >= V ? V : (p.K > k ? static_cast<int>(p.K - k) : 0);
+            if constexpr (GRAD) {
+                float f[V];
+                unpack<T>(as_uint4(a[s]), f);
+                if constexpr (DROP) {
+                    uint32_t dw[4];
+                    p.drop.draws(node, static_cast<uint32_t>(k >> 3), call, dw);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        // (four fp32 columns are one half of a block's eight)
+                        if constexpr (V == 8) f[e] = p.drop.apply(f[e], dw, e);
+                        else f[e] = h ? p.drop.apply(f[e], dw, e + 4) : p.drop.apply(f[e], dw, e);
+                    }
+                }
+                if constexpr (ACT != SAG_ACT_NONE) {
+                    float zf[V];
+                    unpack<T>(as_uint4(z[s]), zf);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) f[e] = times_act_grad<ACT>(f[e], zf[e], p.slope);
+                }
+                if constexpr (V == 8) a[s] = u32x4_t{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+                else a[s] = u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+            }
+            if (left < V) a[s] = keep_first<T>(a[s], left);
+            if constexpr (sizeof(T) == 2) {
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, b[s]),
+                                                              __builtin_bit_cast(bf16x8_t, a[s]), acc, 0, 0, 0);
+            } else {
+                const f32x4_t bb = __builtin_bit_cast(f32x4_t, b[s]), aa = __builtin_bit_cast(f32x4_t, a[s]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bb[q], aa[q], acc, 0, 0, 0);
+            }
+        }
+    }
+    float* mine = part + wave * 32 * kFewPitch;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(mine + l32 * kFewPitch + 8 * q + 4 * h) =
+            make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+    __syncthreads();
+    // units of eight columns, four lanes to a unit, each every fourth wavefront's sum
+    for (int unit = t >> 2; unit < 128; unit += blockDim.x >> 2) {
+        const int r = unit >> 2, u = unit & 3;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.f;
+        for (int v = t & 3; v < waves; v += 4) {
+            const float* src = part + (v * 32 + r) * kFewPitch + u * 8;
+            const float4 lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
+            y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
+            y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            y[e] += __shfl_xor(y[e], 1, 64);
+            y[e] += __shfl_xor(y[e], 2, 64);
+        }
+        const int64_t orow = m0 + r, ocol = n0 + u * 8;
+        const int live = p.N - ocol < 8 ? static_cast<int>(p.N - ocol) : 8;
+        if ((t & 3) || orow >= p.M || live <= 0) continue;
+        if constexpr (!GRAD) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += p.bias && e < live ? p.bias[ocol + e] : 0.f;
+            if (p.z) Eight<T>::put(p.z + orow * p.ldz + ocol, y, live);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = act_value<ACT, T>(y[e], p.slope);
+            if constexpr (DROP) {
+                uint32_t dw[4];
+                p.drop.draws(p.drop.node_of(orow), static_cast<uint32_t>(ocol >> 3), call, dw);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = p.drop.apply(y[e], dw, e);
+            }
+            if (p.res) {
+                Eight<T> rv;
+                rv.load(p.res + orow * p.ldr + ocol, live);
+                float f[8];
+                rv.get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] += f[e];
+            }
+        }
+        Eight<T>::put(p.out + orow * p.ldo + ocol, y, live);
+    }
+}
+
 // Bp[n, k] = B element (k, n) at b[k * sk + n * sn], zero past K and N.
 template <class T>
 __global__ void dense_pack(const T* __restrict__ b, int64_t sk, int64_t sn, int64_t K, int64_t N, int64_t Kt,
@@ -637,6 +800,38 @@ size_t pack_bytes(int64_t K, int64_t N, sag_dtype dt) {
     return static_cast<size_t>(round_up(N, 256) * k_pad(K, dt) * elt_size(dt));
 }
 
+bool few_tiles(int64_t M, int64_t N) { return cdiv(M, 32) * cdiv(N, 32) <= kFewTiles; }
+
+// The product by 32 x 32 tiles; W as it lies (rows of ldw).
+template <class T, bool GRAD>
+sag_status few_run(const char* what, sag_act act, NnArgs<T> p, const T* w, int64_t ldw, sag_dtype dt, hipStream_t s) {
+    p.n_blk = cdiv(p.N, 32);
+    p.m_blk = cdiv(p.M, 32);
+    const int64_t pieces = cdiv(p.K, kRowB / static_cast<int64_t>(sizeof(T)));
+    const int waves = static_cast<int>(pieces < 16 ? pieces : 16);
+    TraceScope trace(trace_enabled() ? shape_name(what, dt == SAG_BF16 ? "bf16" : "f32", p.M, p.K, p.N) : std::string(),
+                     s, elt_size(dt) * (p.M * p.K * (p.az ? 2 : 1) + p.M * p.N * (1 + (p.z ? 1 : 0) + (p.res ? 1 : 0)) + p.K * p.N),
+                     2 * p.M * p.K * p.N);
+    const unsigned grid = static_cast<unsigned>(p.n_blk * p.m_blk);
+    const size_t lds = static_cast<size_t>(waves) * 32 * kFewPitch * 4;
+    sag_status st = SAG_OK;
+    with_act(act, [&](auto ac) {
+        constexpr int ACT = decltype(ac)::value;
+        auto go = [&](auto drop_c) -> sag_status {
+            constexpr bool DROP = decltype(drop_c)::value;
+            static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_few<T, ACT, DROP, GRAD>),
+                                                               hipFuncAttributeMaxDynamicSharedMemorySize, 16 * 32 * kFewPitch * 4);
+            SAG_CHECK_HIP(attr);
+            dense_few<T, ACT, DROP, GRAD><<<grid, waves * 64, lds, s>>>(p, w, ldw);
+            return SAG_OK;
+        };
+        st = p.drop.T ? go(std::true_type{}) : go(std::false_type{});
+    });
+    SAG_TRY(st);
+    SAG_LAUNCH_CHECK();
+    return SAG_OK;
+}
+
 // Packs B ([K, N]; element (k, n) at b[k sk + n sn]) and multiplies.
 template <class T, bool GRAD = false>
 sag_status nn_run(const char* what, sag_act act, NnArgs<T> p, const T* b, int64_t sk, int64_t sn, T* bp, sag_dtype dt,
@@ -674,7 +869,9 @@ sag_status nn_run(const char* what, sag_act act, NnArgs<T> p, const T* b, int64_
 
 template <class T>
 sag_status forward_typed(NnArgs<T> p, const void* W, sag_act act, sag_dtype dt, void* ws, hipStream_t s) {
-    return nn_run<T>("dense", act, p, static_cast<const T*>(W), p.N, 1, static_cast<T*>(ws), dt, s);
+    const T* w = static_cast<const T*>(W);
+    if (few_tiles(p.M, p.N)) return few_run<T, false>("dense", act, p, w, p.N, dt, s);
+    return nn_run<T>("dense", act, p, w, p.N, 1, static_cast<T*>(ws), dt, s);
 }
 
 // ---- backward ------------------------------------------------------------------------------
@@ -786,7 +983,8 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
     const bool from_g = dz_from_g(K, dt), exact = act == SAG_ACT_NONE || act == SAG_ACT_RELU;
     T* hi = static_cast<T*>(w.hi);
     T* lo = exact ? nullptr : static_cast<T*>(w.lo);
-    if (M > 0 && !from_g) {
+    // (the tiled input gradient reads a stored dZ, and so does the weight gradient)
+    if (M > 0 && !from_g && ((dX && !few_tiles(M, K)) || dW || db)) {
         const int64_t blocks = cdiv(M * upr, kThreads);
         if (blocks >= (1 << 24)) return fail(SAG_E_UNSUPPORTED, "dense backward: too many elements for one launch");
         TraceScope trace(trace_enabled() ? shape_name("dense_dz", dt == SAG_BF16 ? "bf16" : "f32", M, N, 0) : std::string(),
@@ -804,7 +1002,11 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
         NnArgs<T> p{};
         p.M = M; p.K = N; p.N = K;
         p.out = dX; p.ldo = ldd;
-        if (from_g) {
+        if (few_tiles(M, K)) {
+            p.a = G; p.lda = ldg; p.az = act == SAG_ACT_NONE ? nullptr : Z; p.ldaz = ldz;
+            p.slope = slope; p.drop = drop;
+            SAG_TRY((few_run<T, true>("dense_dx", act, p, W, N, dt, s)));
+        } else if (from_g) {
             if constexpr (sizeof(T) == 2) {
                 p.a = G; p.lda = ldg; p.az = act == SAG_ACT_NONE ? nullptr : Z; p.ldaz = ldz;
                 p.slope = slope; p.drop = drop;
