@@ -651,7 +651,8 @@ sag_status sag_dropout(const void* X, int64_t ldx, int64_t n, int64_t d, sag_dty
  * backward call needs it unless act is SAG_ACT_NONE); Out: [M, N].  X, W, R,
  * Z and Out of type dt, sums in fp32, each output rounded once (act sees the
  * unrounded Z).  K, N >= 1; M may be 0.  Out may be R (same pointer and ld).
- * K and N have no limit below 2^24. */
+ * K and N have no limit below 2^24.  A product of few tiles needs no
+ * workspace (the query returns 0; ws may be NULL). */
 size_t sag_dense_forward_workspace_bytes(int64_t M, int64_t K, int64_t N, sag_dtype dt);
 sag_status sag_dense_layer_forward(int64_t M, const void* X, int64_t ldx, int64_t K, const void* W, const float* b,
                                    int64_t N, sag_act act, float slope, const sag_drop* drop, const void* R,

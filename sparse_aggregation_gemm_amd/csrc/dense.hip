@@ -1047,8 +1047,7 @@ sag_status check_sizes(const char* who, int64_t M, int64_t K, int64_t N, sag_act
 using namespace sag;
 
 extern "C" size_t sag_dense_forward_workspace_bytes(int64_t M, int64_t K, int64_t N, sag_dtype dt) {
-    (void)M;
-    if (K < 1 || N < 1 || (dt != SAG_F32 && dt != SAG_BF16)) return 0;
+    if (M < 0 || K < 1 || N < 1 || (dt != SAG_F32 && dt != SAG_BF16) || few_tiles(M, N)) return 0;
     return pack_bytes(K, N, dt);
 }
 
@@ -1066,7 +1065,8 @@ extern "C" sag_status sag_dense_layer_forward(int64_t M, const void* X, int64_t 
     DropArgs da;
     SAG_TRY(make_drop("dense forward", drop, M, &da));
     if (M == 0) return SAG_OK;
-    if (!ws || !aligned16(ws) || ws_bytes < sag_dense_forward_workspace_bytes(M, K, N, dt))
+    const size_t need = sag_dense_forward_workspace_bytes(M, K, N, dt);
+    if (need && (!ws || !aligned16(ws) || ws_bytes < need))
         return fail(SAG_E_WORKSPACE, "dense forward: workspace too small");
     hipStream_t s = static_cast<hipStream_t>(stream);
     auto go = [&](auto tag) {

@@ -40,7 +40,7 @@ def padded_ld(d: int, dtype: torch.dtype) -> int:
     """Row pitch in elements: rows wider than 64 bytes span whole 128-byte
     cache lines (a gathered row then touches as few lines as possible),
     narrower rows are padded to 16 bytes."""
-    es = torch.empty(0, dtype=dtype).element_size()
+    es = dtype.itemsize
     nbytes = max(d, 1) * es
     line = 128 if nbytes > 64 else 16
     return (nbytes + line - 1) // line * line // es
@@ -789,7 +789,7 @@ def _need(what: str, t, shape, dtype, device) -> None:
         return
     if t.dtype != dtype:
         raise TypeError(f"{what} is {t.dtype}; the call takes {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}; the call takes {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}; the call runs on {device}")
@@ -808,22 +808,31 @@ def _row_vec(what: str, t, n: int, device):
     return None if t is None else t.contiguous()
 
 
-class _on:
-    """Makes `device` the current one for a launch on it."""
+def _opt_ld(t) -> int:
+    return 0 if t is None else _ld(t)
 
-    def __init__(self, device):
-        self.device = device
-        self.back = None
 
-    def __enter__(self):
-        if self.device.type == "cuda" and self.device.index is not None \
-                and torch.cuda.current_device() != self.device.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.device)
+def _opt_ws(nbytes: int, ws, device):
+    """The caller's workspace where it is large enough, a fresh one, or None
+    for a call that needs none."""
+    if nbytes == 0:
+        return None
+    return ws if ws is not None and ws.numel() >= nbytes else _ws(nbytes, device)
 
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+
+def _launch(name: str, device, *args) -> None:
+    """Calls an entry point on `device` (made the current one for the launch)
+    and its current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: the operands must be on the GPU")
+    fn = getattr(L.lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    if st:
+        L.check(name, st)
 
 
 @dataclass(frozen=True)
@@ -867,11 +876,9 @@ def dropout(X, drop: Drop, addend=None, Out=None):
     _need("dropout Out", Out, X.shape, X.dtype, X.device)
     if Out is None:
         Out = empty_dense(X.shape[0], X.shape[1], X.dtype, X.device)
-    d = _drop(drop, X.shape[0], X.device)
-    with _on(X.device):
-        st = L.lib().sag_dropout(_ptr(X), _ld(X), X.shape[0], X.shape[1], dtype_code(X.dtype), d, _ptr(addend),
-                                 _ld(addend) if addend is not None else 0, _ptr(Out), _ld(Out), _stream(X.device))
-    L.check("sag_dropout", st)
+    n, width = X.shape
+    _launch("sag_dropout", X.device, X.data_ptr(), _ld(X), n, width, _DT[X.dtype], _drop(drop, n, X.device), _ptr(addend),
+            _opt_ld(addend), Out.data_ptr(), _ld(Out))
     return Out
 
 
@@ -903,8 +910,7 @@ def dense_layer_forward(X, W, b=None, act="relu", slope=0.01, drop: Drop | None 
     d = _drop(drop, M, dev)
     if want_z is None:
         want_z = act != "none"
-    lib = L.lib()
-    dt = dtype_code(X.dtype)
+    dt = _DT[X.dtype]
     W = W.contiguous()
     if Out is None:
         Out = empty_dense(M, N, X.dtype, dev)
@@ -912,15 +918,11 @@ def dense_layer_forward(X, W, b=None, act="relu", slope=0.01, drop: Drop | None 
         Z = None
     elif Z is None:
         Z = empty_dense(M, N, X.dtype, dev)
-    nws = lib.sag_dense_forward_workspace_bytes(M, K, N, dt)
-    if ws is None or ws.numel() < nws:
-        ws = _ws(nws, dev)
-    with _on(dev):
-        st = lib.sag_dense_layer_forward(M, _ptr(X), _ld(X), K, _ptr(W), _ptr(b), N, code, float(slope), d,
-                                         _ptr(residual), _ld(residual) if residual is not None else 0, dt, _ptr(Z),
-                                         _ld(Z) if Z is not None else 0, _ptr(Out), _ld(Out), _ptr(ws), ws.numel(),
-                                         _stream(dev))
-    L.check("sag_dense_layer_forward", st)
+    nws = L.lib().sag_dense_forward_workspace_bytes(M, K, N, dt)
+    ws = _opt_ws(nws, ws, dev)
+    _launch("sag_dense_layer_forward", dev, M, X.data_ptr(), _ld(X), K, W.data_ptr(), _ptr(b), N, code, slope, d,
+            _ptr(residual), _opt_ld(residual), dt, _ptr(Z), _opt_ld(Z), Out.data_ptr(), _ld(Out), _ptr(ws),
+            0 if ws is None else ws.numel())
     return Out, Z, DenseCtx(X, W, act, float(slope), drop)
 
 
@@ -941,8 +943,7 @@ def dense_layer_backward(ctx: DenseCtx, Z, G_out, want_dX=True, want_db=True, dX
     _need("dense_layer_backward G_out", G_out, (M, N), X.dtype, dev)
     _need("dense_layer_backward dX", dX, (M, K), X.dtype, dev)
     d = _drop(ctx.drop, M, dev)
-    lib = L.lib()
-    dt = dtype_code(X.dtype)
+    dt = _DT[X.dtype]
     W = W.contiguous()
     dW = torch.empty((K, N), dtype=torch.float32, device=dev)
     db = torch.empty(N, dtype=torch.float32, device=dev) if want_db else None
@@ -950,15 +951,11 @@ def dense_layer_backward(ctx: DenseCtx, Z, G_out, want_dX=True, want_db=True, dX
         dX = None
     elif dX is None:
         dX = empty_dense(M, K, X.dtype, dev)
-    nws = lib.sag_dense_backward_workspace_bytes(M, K, N, dt)
-    if ws is None or ws.numel() < nws:
-        ws = _ws(nws, dev)
-    with _on(dev):
-        st = lib.sag_dense_layer_backward(M, _ptr(X), _ld(X), K, _ptr(W), N, code, ctx.slope, d, _ptr(Z),
-                                          _ld(Z) if Z is not None else 0, _ptr(G_out), _ld(G_out), _ptr(dW), _ptr(db),
-                                          _ptr(dX), _ld(dX) if dX is not None else 0, dt, _ptr(ws), ws.numel(),
-                                          _stream(dev))
-    L.check("sag_dense_layer_backward", st)
+    nws = L.lib().sag_dense_backward_workspace_bytes(M, K, N, dt)
+    ws = _opt_ws(nws, ws, dev)
+    _launch("sag_dense_layer_backward", dev, M, X.data_ptr(), _ld(X), K, W.data_ptr(), N, code, ctx.slope, d, _ptr(Z),
+            _opt_ld(Z), G_out.data_ptr(), _ld(G_out), dW.data_ptr(), _ptr(db), _ptr(dX), _opt_ld(dX), dt, _ptr(ws),
+            0 if ws is None else ws.numel())
     return dW, db, dX
 
 
@@ -1002,20 +999,14 @@ def group_norm_forward(X, groups=1, weight=None, bias=None, seg=None, eps=1e-5, 
     dev, n, d = X.device, X.shape[0], X.shape[1]
     _need("group_norm_forward Out", Out, X.shape, X.dtype, dev)
     code = _act_code(act)
-    lib = L.lib()
-    dt = dtype_code(X.dtype)
+    dt = _DT[X.dtype]
     if Out is None:
         Out = empty_dense(n, d, X.dtype, dev, fill=None if seg is None else 0.0)
-    mean = torch.empty((n_seg, groups), dtype=torch.float32, device=dev)
-    rstd = torch.empty((n_seg, groups), dtype=torch.float32, device=dev)
-    nws = lib.sag_group_norm_forward_workspace_bytes(n, d, groups, n_seg, dt)
-    if ws is None or ws.numel() < nws:
-        ws = _ws(nws, dev)
-    with _on(dev):
-        st = lib.sag_group_norm_forward(_ptr(X), _ld(X), n, d, groups, _ptr(seg), n_seg, _ptr(weight), _ptr(bias),
-                                        float(eps), code, float(slope), dt, _ptr(Out), _ld(Out), _ptr(mean), _ptr(rstd),
-                                        _ptr(ws), ws.numel(), _stream(dev))
-    L.check("sag_group_norm_forward", st)
+    mean, rstd = torch.empty((2, n_seg, groups), dtype=torch.float32, device=dev).unbind(0)
+    nws = L.lib().sag_group_norm_forward_workspace_bytes(n, d, groups, n_seg, dt)
+    ws = _opt_ws(max(nws, 1), ws, dev)
+    _launch("sag_group_norm_forward", dev, X.data_ptr(), _ld(X), n, d, groups, _ptr(seg), n_seg, _ptr(weight), _ptr(bias),
+            eps, code, slope, dt, Out.data_ptr(), _ld(Out), mean.data_ptr(), rstd.data_ptr(), ws.data_ptr(), ws.numel())
     return Out, GroupNormCtx(X, groups, weight, bias, seg, mean, rstd, act, float(slope))
 
 
@@ -1030,24 +1021,18 @@ def group_norm_backward(ctx: GroupNormCtx, G_out, want_dX=True, dX=None, ws=None
     _need("group_norm_backward mean", ctx.mean, (n_seg, ctx.groups), torch.float32, dev)
     _need("group_norm_backward rstd", ctx.rstd, (n_seg, ctx.groups), torch.float32, dev)
     code = _act_code(ctx.act)
-    lib = L.lib()
-    dt = dtype_code(X.dtype)
+    dt = _DT[X.dtype]
     mean, rstd = ctx.mean.contiguous(), ctx.rstd.contiguous()
-    dw = torch.empty(d, dtype=torch.float32, device=dev)
-    dv = torch.empty(d, dtype=torch.float32, device=dev)
+    dw, dv = torch.empty((2, d), dtype=torch.float32, device=dev).unbind(0)
     if not want_dX:
         dX = None
     elif dX is None:
         dX = empty_dense(n, d, X.dtype, dev, fill=None if seg is None else 0.0)
-    nws = lib.sag_group_norm_backward_workspace_bytes(n, d, ctx.groups, n_seg, dt)
-    if ws is None or ws.numel() < nws:
-        ws = _ws(nws, dev)
-    with _on(dev):
-        st = lib.sag_group_norm_backward(_ptr(X), _ld(X), n, d, ctx.groups, _ptr(seg), n_seg, _ptr(weight), _ptr(bias),
-                                         code, float(ctx.slope), _ptr(mean), _ptr(rstd), _ptr(G_out), _ld(G_out),
-                                         _ptr(dw), _ptr(dv), _ptr(dX), _ld(dX) if dX is not None else 0, dt, _ptr(ws),
-                                         ws.numel(), _stream(dev))
-    L.check("sag_group_norm_backward", st)
+    nws = L.lib().sag_group_norm_backward_workspace_bytes(n, d, ctx.groups, n_seg, dt)
+    ws = _opt_ws(max(nws, 1), ws, dev)
+    _launch("sag_group_norm_backward", dev, X.data_ptr(), _ld(X), n, d, ctx.groups, _ptr(seg), n_seg, _ptr(weight),
+            _ptr(bias), code, ctx.slope, mean.data_ptr(), rstd.data_ptr(), G_out.data_ptr(), _ld(G_out), dw.data_ptr(),
+            dv.data_ptr(), _ptr(dX), _opt_ld(dX), dt, ws.data_ptr(), ws.numel())
     return dw, dv, dX
 
 

@@ -41,6 +41,15 @@ def test_dropout_binding():
         sag.dropout(z(4, 8), replace(D, counter=torch.zeros(1, dtype=torch.int64)))
 
 
+def test_operands_must_be_on_the_gpu():
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        sag.dropout(z(4, 8), D)
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        sag.dense_layer_forward(z(6, 8), z(8, 5))
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        sag.group_norm_forward(z(6, 8), 2)
+
+
 def test_dense_binding():
     X, W = z(6, 8), z(8, 5)
     with pytest.raises(ValueError, match="W has shape"):
@@ -132,8 +141,11 @@ def test_dense_abi():
     assert fwd(ldo=6) == L.SAG_E_INVALID and fwd(N=5, ldo=6) == L.SAG_E_ALIGN
     assert fwd(r=ctypes.c_void_p(4)) == L.SAG_E_ALIGN
     assert fwd(dr=drop(p=2.0)) == L.SAG_E_INVALID
-    assert fwd(nb=16) == L.SAG_E_WORKSPACE and fwd(ws=None) == L.SAG_E_WORKSPACE
-    assert fwd(ws=ctypes.c_void_p(8)) == L.SAG_E_WORKSPACE
+    big = 100_000                                  # rows of more tiles than need no workspace
+    assert fwd(M=big, nb=16) == L.SAG_E_WORKSPACE and fwd(M=big, ws=None) == L.SAG_E_WORKSPACE
+    assert fwd(M=big, ws=ctypes.c_void_p(8)) == L.SAG_E_WORKSPACE
+    assert lib.sag_dense_forward_workspace_bytes(4, 8, 8, 0) == 0
+    assert lib.sag_dense_forward_workspace_bytes(big, 8, 8, 0) > 0
     assert fwd(M=0) == L.SAG_OK
 
     def bwd(M=4, x=fake, K=8, w=fake, N=8, act=1, zz=fake, g=fake, dw=fake, db=fake, dx=fake, dt=0, nb=BIG):
