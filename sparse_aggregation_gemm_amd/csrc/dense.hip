@@ -275,23 +275,27 @@ __global__ __launch_bounds__((BN == 256 ? 512 : 256), GRAD ? (BN == 256 ? 4 : 3)
                 const int r = (wn * NB + j) * 32 + l32;
                 b[j] = load16(Bs + r * kRowB + (((2 * s + h) ^ swz(r)) << 4));
             }
+            // (independent sums in turn: a product waits for the one before it into the same sum)
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int i = 0; i < MB; ++i)
+                for (int i = 0; i < MB; ++i)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    if constexpr (sizeof(T) == 2) {
+                    for (int j = 0; j < NB; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, b[j]),
                                                                              __builtin_bit_cast(bf16x8_t, a[i]),
                                                                              acc[i][j], 0, 0, 0);
-                    } else {
-                        // unit h holds k 4h .. 4h + 3 of the step: product q pairs k q with k 4 + q
-                        const f32x4_t bb = __builtin_bit_cast(f32x4_t, b[j]);
-                        const f32x4_t aa = __builtin_bit_cast(f32x4_t, a[i]);
+            } else {
+                // unit h holds k 4h .. 4h + 3 of the step: product q pairs k q with k 4 + q
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(bb[q], aa[q], acc[i][j], 0, 0, 0);
-                    }
-                }
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(f32x4_t, b[j])[q],
+                                                                             __builtin_bit_cast(f32x4_t, a[i])[q],
+                                                                             acc[i][j], 0, 0, 0);
+            }
         }
         __syncthreads();
     }

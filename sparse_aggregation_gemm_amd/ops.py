@@ -22,7 +22,13 @@ _DT = {torch.float32: L.SAG_F32, torch.bfloat16: L.SAG_BF16}
 _NORM = {"gcn": L.SAG_NORM_GCN, "mean": L.SAG_NORM_MEAN, "none": L.SAG_NORM_NONE}
 
 
+# (the raw handle costs 0.1 us where building a Stream object costs 1.9)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
