@@ -95,12 +95,13 @@ struct Eight {
 };
 
 // The derivative of GELU and SiLU at a bf16 argument, from a table in LDS:
-// act'(z) - 1/2 is odd, so the table holds it for the 1664 bf16 values from
-// 2^-8 up to 32, beyond which it is 1/2 in fp32; below 2^-8 it is its slope
-// at 0 times z (to 2e-8).  A lookup is 11 operations and one LDS read against
-// 25 for the formula, and the gradient kernels are bound by their arithmetic:
-// 1.04 and 1.16 ms without it at 2.45M x 256 x 256 (3.8 GB each).  NaN takes
-// the branch of small z and stays NaN.
+// act'(z) - 1/2 is odd, so act'(z) = 1/2 + z r(|z|) with r smooth down to 0,
+// and the table holds r (times the dropout scale) for the 1664 bf16 values
+// from 2^-8, below which r is constant to 5e-6 of itself, up to 32, beyond
+// which act' is that of 32 in fp32.  A lookup is seven operations and one LDS
+// read against 25 for the formula, and the gradient kernels are bound by
+// their arithmetic.  NaN stays NaN, and an infinite z gives NaN as it does in
+// the formula.
 constexpr int kTabSize = 1664;
 constexpr uint32_t kTabFirst = 0x3B80u;     // 2^-8
 
@@ -108,22 +109,23 @@ template <int ACT>
 constexpr bool uses_table() { return ACT == SAG_ACT_GELU || ACT == SAG_ACT_SILU; }
 
 template <int ACT>
-__device__ __forceinline__ void build_table(float* tab, int t, int threads) {
+__device__ __forceinline__ void build_table(float* tab, float scale, int t, int threads) {
     if constexpr (uses_table<ACT>()) {
-        for (int i = t; i < kTabSize; i += threads)
-            tab[i] = act_grad<ACT>(__uint_as_float((kTabFirst + i) << 16), 0.f) - 0.5f;
+        for (int i = t; i < kTabSize; i += threads) {
+            const float a = __uint_as_float((kTabFirst + i) << 16);
+            tab[i] = (act_grad<ACT>(a, 0.f) - 0.5f) * scale / a;
+        }
         __syncthreads();
     }
 }
 
-// act'(z) for the bf16 bits in the high half of `zbits` (the low half is 0).
-template <int ACT>
-__device__ __forceinline__ float table_grad(const float* tab, uint32_t zbits) {
+// scale act'(z) for the bf16 bits in the high half of `zbits` (the low half
+// is 0); half = scale / 2.
+__device__ __forceinline__ float table_grad(const float* tab, uint32_t zbits, float half) {
     const float z = __uint_as_float(zbits);
-    const uint32_t i = ((zbits >> 16) & 0x7fffu) - kTabFirst;
-    const float h = tab[i < kTabSize - 1 ? i : kTabSize - 1];
-    const float near0 = z * (ACT == SAG_ACT_GELU ? 0.79788456080286536f : 0.5f);
-    return 0.5f + (fabsf(z) >= 0x1p-8f ? copysignf(h, z) : near0);
+    uint32_t i = (zbits >> 16) & 0x7fffu;
+    i = i < kTabFirst ? kTabFirst : (i > kTabFirst + kTabSize - 1 ? kTabFirst + kTabSize - 1 : i);
+    return fmaf(__builtin_amdgcn_fmed3f(z, -32.f, 32.f), tab[i - kTabFirst], fmaf(z, 0.f, half));
 }
 
 // The eight values of dZ = act'(Z) dropout(G) from the vectors of G and Z.
@@ -132,6 +134,7 @@ __device__ __forceinline__ void dz_of(u32x4_t g, u32x4_t z, const float* tab, co
                                       uint32_t block, uint32_t call, float slope, float (&f)[8]) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if constexpr (DROP) drop.draws(node, block, call, w);
+    const float half = DROP ? 0.5f * drop.scale : 0.5f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         // (two at a time: all eight's temporaries at once cost a wavefront a SIMD)
@@ -139,9 +142,10 @@ __device__ __forceinline__ void dz_of(u32x4_t g, u32x4_t z, const float* tab, co
 #pragma unroll
         for (int e = 2 * q; e < 2 * q + 2; ++e) {
             float x = __uint_as_float(e & 1 ? g[q] & 0xffff0000u : g[q] << 16);
-            if constexpr (DROP) x = drop.apply(x, w, e);
+            // (the table has the dropout scale)
+            if constexpr (DROP) x = uses_table<ACT>() ? drop.mask(x, w, e) : drop.apply(x, w, e);
             const uint32_t zb = e & 1 ? z[q] & 0xffff0000u : z[q] << 16;
-            if constexpr (uses_table<ACT>()) x *= table_grad<ACT>(tab, zb);
+            if constexpr (uses_table<ACT>()) x *= table_grad(tab, zb, half);
             else if constexpr (ACT != SAG_ACT_NONE) x = times_act_grad<ACT>(x, __uint_as_float(zb), slope);
             f[e] = x;
         }
@@ -195,7 +199,7 @@ __global__ __launch_bounds__((BN == 256 ? 512 : 256), GRAD ? (BN == 256 ? 4 : 3)
     unsigned char* Bs = lds + kBM * kRowB;
 
     __shared__ float tab[GRAD && uses_table<ACT>() ? kTabSize : 1];
-    if constexpr (GRAD) build_table<ACT>(tab, threadIdx.x, kThreads);
+    if constexpr (GRAD) build_table<ACT>(tab, DROP ? p.drop.scale : 1.f, threadIdx.x, kThreads);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wm = wave / WN, wn = wave % WN;
     const int h = lane >> 5, l32 = lane & 31;
@@ -606,7 +610,7 @@ __global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
     constexpr int STAGE = SX + (LO ? 2 : 1) * SZ;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     float* tab = reinterpret_cast<float*>(lds + 2 * STAGE);
-    if constexpr (FROM_G) build_table<ACT>(tab, threadIdx.x, kTnThreads);
+    if constexpr (FROM_G) build_table<ACT>(tab, DROP ? p.drop.scale : 1.f, threadIdx.x, kTnThreads);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wk = wave >> 2, wn = wave & 3;
     // the blocks of one chunk next to each other on one XCD

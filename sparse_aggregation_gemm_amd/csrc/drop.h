@@ -40,9 +40,10 @@ struct DropArgs {
     // x of column e (of the eight) after dropout; a dropped NaN or infinity
     // is 0.  (A draw u in the high half and anything below it: u < T where
     // the word is at most 65536 T - 1, so the odd columns need no shift.)
-    __device__ __forceinline__ float apply(float x, const uint32_t (&w)[4], int e) const {
+    __device__ __forceinline__ float apply(float x, const uint32_t (&w)[4], int e) const { return mask(x * scale, w, e); }
+    __device__ __forceinline__ float mask(float x, const uint32_t (&w)[4], int e) const {
         const uint32_t u = (e & 1) ? w[e / 2] : w[e / 2] << 16;
-        return u > last ? x * scale : 0.f;
+        return u > last ? x : 0.f;
     }
 };
 
