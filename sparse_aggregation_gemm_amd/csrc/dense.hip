@@ -142,11 +142,11 @@ __device__ __forceinline__ void dz_of(u32x4_t g, u32x4_t z, const float* tab, co
 #pragma unroll
         for (int e = 2 * q; e < 2 * q + 2; ++e) {
             float x = __uint_as_float(e & 1 ? g[q] & 0xffff0000u : g[q] << 16);
-            // (the table has the dropout scale)
-            if constexpr (DROP) x = uses_table<ACT>() ? drop.mask(x, w, e) : drop.apply(x, w, e);
             const uint32_t zb = e & 1 ? z[q] & 0xffff0000u : z[q] << 16;
             if constexpr (uses_table<ACT>()) x *= table_grad(tab, zb, half);
             else if constexpr (ACT != SAG_ACT_NONE) x = times_act_grad<ACT>(x, __uint_as_float(zb), slope);
+            // (last: a dropped value is 0 whatever G and Z are; the table has the scale)
+            if constexpr (DROP) x = uses_table<ACT>() ? drop.mask(x, w, e) : drop.apply(x, w, e);
             f[e] = x;
         }
     }
@@ -441,6 +441,12 @@ __global__ __launch_bounds__(1024) void dense_few(NnArgs<T> p, const T* __restri
             if constexpr (GRAD) {
                 float f[V];
                 unpack<T>(as_uint4(a[s]), f);
+                if constexpr (ACT != SAG_ACT_NONE) {
+                    float zf[V];
+                    unpack<T>(as_uint4(z[s]), zf);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) f[e] = times_act_grad<ACT>(f[e], zf[e], p.slope);
+                }
                 if constexpr (DROP) {
                     uint32_t dw[4];
                     p.drop.draws(node, static_cast<uint32_t>(k >> 3), call, dw);
@@ -450,12 +456,6 @@ __global__ __launch_bounds__(1024) void dense_few(NnArgs<T> p, const T* __restri
                         if constexpr (V == 8) f[e] = p.drop.apply(f[e], dw, e);
                         else f[e] = h ? p.drop.apply(f[e], dw, e + 4) : p.drop.apply(f[e], dw, e);
                     }
-                }
-                if constexpr (ACT != SAG_ACT_NONE) {
-                    float zf[V];
-                    unpack<T>(as_uint4(z[s]), zf);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) f[e] = times_act_grad<ACT>(f[e], zf[e], p.slope);
                 }
                 if constexpr (V == 8) a[s] = u32x4_t{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
                 else a[s] = u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
@@ -549,17 +549,17 @@ __global__ __launch_bounds__(kThreads) void dense_dz(int64_t M, int64_t N, int64
     if constexpr (ACT != SAG_ACT_NONE) zv.load(z + row * ldz + col, live);
     float f[8];
     gv.get(f);
-    if (drop.T) {
-        uint32_t dw[4];
-        drop.draws(drop.node_of(row), static_cast<uint32_t>(u), drop.call_now(), dw);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = drop.apply(f[e], dw, e);
-    }
     if constexpr (ACT != SAG_ACT_NONE) {
         float zf[8];
         zv.get(zf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = times_act_grad<ACT>(f[e], zf[e], slope);
+    }
+    if (drop.T) {
+        uint32_t dw[4];
+        drop.draws(drop.node_of(row), static_cast<uint32_t>(u), drop.call_now(), dw);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = drop.apply(f[e], dw, e);
     }
     Eight<T>::put(hi + row * ldh + col, f, live);
     if (lo) {

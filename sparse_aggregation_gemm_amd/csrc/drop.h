@@ -141,7 +141,7 @@ __device__ __forceinline__ float act_value(float z, float slope) {
         // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
         float e;
         const float q = normal_tail<sizeof(T) == 4>(z, e);
-        return fmaf(-fabsf(z), q, z < 0.f ? 0.f : z);
+        return fmaf(-fminf(fabsf(z), 32.f), q, z < 0.f ? 0.f : z);   // (q is 0 there, and infinity stays)
     } else if constexpr (ACT == SAG_ACT_SILU) return z * sigmoid(z);
     else return z;
 }

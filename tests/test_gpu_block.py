@@ -3,8 +3,7 @@ oracle on the same stored inputs.
 
 Bounds.  u = 2^-24 (half a step of fp32) and ut = finfo(dtype).eps / 2 for the
 one rounding of an output.  An activation or its derivative is taken to cost
-16 u of its argument's size (the library functions are within a few units in
-the last place), a sum of n terms n u of the sum of their sizes (whatever
+16 u of its argument's size (and the GELU of a bf16 result what fit() says), a sum of n terms n u of the sum of their sizes (whatever
 the order).  These are worst cases; the exact-integer tests below leave no room."""
 import numpy as np
 import pytest
@@ -22,6 +21,14 @@ U = 2.0 ** -24
 TD = {"f32": torch.float32, "bf16": torch.bfloat16}
 UT = {k: torch.finfo(v).eps / 2 for k, v in TD.items()}
 LIP = 1.13                       # largest slope of any of the activations
+
+
+def fit(kind, dt, z):
+    """What GELU's tail costs where the result is rounded to bf16: z Phi(z) is
+    max(z, 0) - |z| (1 - Phi(|z|)), and the five-term fit of the second factor
+    is off by 3.1e-5 of it at most (its polynomial against log_ndtr in 64 bits
+    on [0, 14]: 3.110e-5); at most 5.3e-6, where half a step of bf16 at 1 is 3.9e-3."""
+    return 3.2e-5 * np.abs(z) * torch.special.ndtr(torch.from_numpy(-np.abs(z))).numpy() if kind == "gelu" and dt == "bf16" else 0.0
 
 
 def mat(g, rows, d, dt, integers=False, scale=1.0):
@@ -153,7 +160,7 @@ def test_dense_forward(dt, M, K, N, kind, p, res):
     Z, Out = ob.dense_forward(x, w, bb, kind, 0.1, f, f64(R) if res else None)
     ez = (K + 1) * U * (np.abs(x) @ np.abs(w) + np.abs(bb))
     within(z, Z, ez + UT[dt] * np.abs(Z) + 1e-30)
-    eo = f * (LIP * ez + 16 * U * np.abs(Z)) + 3 * U * np.abs(f * Z) + U * np.abs(Out)
+    eo = f * (LIP * ez + 16 * U * np.abs(Z) + fit(kind, dt, Z)) + 3 * U * np.abs(f * Z) + U * np.abs(Out)
     within(out, Out, eo + UT[dt] * (np.abs(Out) + eo) + 1e-30)
     # the same call again, without Z: the same bits
     out2, z2, _ = sag.dense_layer_forward(X, W, b, act=kind, slope=0.1, drop=drop, residual=R, want_z=False)
@@ -325,7 +332,8 @@ def test_norm_forward(dt, n, d, groups, seg, kind):
     for i in range(len(seg_h) - 1):
         r = slice(seg_h[i], seg_h[i + 1])
         xw = np.abs((x[r] - np.repeat(m32[i], D)) * np.repeat(r32[i], D) * f64(w))
-        tol[r] = LIP * 5 * U * (xw + np.abs(f64(b))) + 16 * U * (xw + np.abs(f64(b)))
+        z = (x[r] - np.repeat(m32[i], D)) * np.repeat(r32[i], D) * f64(w) + f64(b)
+        tol[r] = LIP * 5 * U * (xw + np.abs(f64(b))) + 16 * U * (xw + np.abs(f64(b))) + fit(kind, dt, z)
     within(out, ref, tol * 1.01 + UT[dt] * np.abs(ref))
     # rows of no graph were left as they were
     own = np.zeros(n, bool)
