@@ -35,6 +35,8 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kHold = 4;              // rows a thread holds at once
 constexpr int64_t kMaxChunks = 2048, kMaxGraphBlocks = 2048;   // eight workgroups a CU each
+constexpr int kWaveHold = 16;         // rows a thread of a wavefront's graph
+constexpr int64_t kManyGraphs = 512;  // from here on the shortest graphs are wavefronts'
 constexpr int kShort = 32;            // a graph of so many rows a thread is one workgroup's
 
 struct NormArgs {
@@ -54,10 +56,12 @@ struct NormArgs {
     int64_t ldg;
     float2* piece;                // [n_chunks + n_seg][groups]
     float2* stat;                 // backward: [n_seg][groups] means of h and h xhat
-    float* col;                   // backward: [graph_blocks + chunk_blocks][2][d] column sums
+    float* col;                   // backward: [the first pass's workgroups][2][d] column sums
     int64_t rows_per_chunk, n_chunks;
     int64_t short_rows;           // graphs of up to so many rows are done whole
-    int64_t graph_blocks;         // the first pass's workgroups for short graphs, before the chunks'
+    int64_t wave_rows;            // of these, up to so many by a wavefront
+    int64_t graph_blocks, wave_blocks;   // the first pass's workgroups for short graphs; the chunks' follow
+    int lanes_per_group, lanes_per_slots;   // in the sums over a group: powers of two
     int64_t seg_per_block;        // graphs and groups per block of the joining kernel
     int grp_per_block;
     int tx, ty;                   // threads across the columns' vectors and down the rows
@@ -122,23 +126,18 @@ __device__ __forceinline__ u32x4_t load16(const void* p) { return *reinterpret_c
 template <class T>
 __device__ __forceinline__ void unpack_vec(u32x4_t v, float (&f)[Vec<T>::N]) { unpack<T>(as_uint4(v), f); }
 
-// Rows r, r + ty, ... below hi (a piece has fewer than 2^31).
-__device__ __forceinline__ uint32_t rows_of(const NormArgs& a, int64_t r, int64_t hi) {
-    return r < hi ? static_cast<uint32_t>(hi - r - 1) / static_cast<uint32_t>(a.ty) + 1u : 0u;
-}
-
 // f(vectors of x and, with TWO, of y) for the `cnt` rows of a thread, `sx`
-// (`sy`) bytes apart, four rows' loads at a time.  Pointers only ever move by
+// (`sy`) bytes apart, H rows' loads at a time.  Pointers only ever move by
 // the step, and rows past the last cost no arithmetic: a graph of 25 rows is
 // short enough for address products and selects to take longer than its data.
-template <bool TWO, class F>
+template <bool TWO, int H = kHold, class F>
 __device__ __forceinline__ void each_row(const void* x, int64_t sx, const void* y, int64_t sy, int64_t cnt, F&& f) {
     const char* px = static_cast<const char*>(x);
     const char* py = static_cast<const char*>(y);
-    for (; cnt >= kHold; cnt -= kHold) {
-        u32x4_t q[kHold], g[kHold];
+    for (; cnt >= H; cnt -= H) {
+        u32x4_t q[H], g[H];
 #pragma unroll
-        for (int i = 0; i < kHold; ++i) {
+        for (int i = 0; i < H; ++i) {
             q[i] = load16(px);
             px += sx;
             if constexpr (TWO) {
@@ -147,12 +146,12 @@ __device__ __forceinline__ void each_row(const void* x, int64_t sx, const void* 
             }
         }
 #pragma unroll
-        for (int i = 0; i < kHold; ++i) f(q[i], g[i]);
+        for (int i = 0; i < H; ++i) f(q[i], g[i]);
     }
     if (cnt > 0) {
-        u32x4_t q[kHold - 1], g[kHold - 1];
+        u32x4_t q[H - 1], g[H - 1];
 #pragma unroll
-        for (int i = 0; i < kHold - 1; ++i) {
+        for (int i = 0; i < H - 1; ++i) {
             q[i] = load16(px);
             if constexpr (TWO) g[i] = load16(py);
             if (i + 1 < cnt) {
@@ -161,7 +160,7 @@ __device__ __forceinline__ void each_row(const void* x, int64_t sx, const void* 
             }
         }
 #pragma unroll
-        for (int i = 0; i < kHold - 1; ++i)
+        for (int i = 0; i < H - 1; ++i)
             if (i < cnt) f(q[i], g[i]);
     }
 }
@@ -179,50 +178,83 @@ __host__ __device__ inline Slots slots_of(int64_t d, int gd, int tx, int V) {
     return COL ? Slots{static_cast<int>(d), gd} : Slots{tx, gd / V};
 }
 
+// LDS for the sums per group: two planes to a team.
+__host__ __device__ inline int stat_floats(const NormArgs& a) { return (a.wave_blocks ? 8 : 2) * a.groups; }
+
+// The threads that do a graph or a piece together: a workgroup, or a
+// wavefront for the shortest graphs.
+template <int SZ>
+struct Team {
+    int tid, tx, ty, rows;      // the thread's column vector and row, and the team's rows of threads
+    bool on;                    // false: past the last row of threads
+    float *sums, *gs;           // LDS: [N][rows][slots], [2][groups]
+    // sh: N * a.ty * slots floats for the sums, then stat_floats(a)
+    __device__ __forceinline__ Team(const NormArgs& a, const Slots& sl, int n_sums, float* sh) {
+        const int wave = SZ == 64 ? static_cast<int>(threadIdx.x) >> 6 : 0;
+        tid = SZ == 64 ? static_cast<int>(threadIdx.x) & 63 : static_cast<int>(threadIdx.x);
+        rows = SZ == 64 ? 64 / a.tx : a.ty;
+        ty = static_cast<int>(static_cast<uint32_t>(tid) / static_cast<uint32_t>(a.tx));
+        tx = tid - ty * a.tx;
+        on = ty < rows;
+        sums = sh + n_sums * wave * rows * sl.n;
+        gs = sh + n_sums * a.ty * sl.n + 2 * wave * a.groups;
+    }
+    // Orders the team's LDS accesses before and after.
+    static __device__ __forceinline__ void sync() {
+        if constexpr (SZ == 64) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            __syncthreads();
+        }
+    }
+    // Rows lo + ty, lo + ty + rows, ... below hi (a piece has fewer than 2^31).
+    __device__ __forceinline__ uint32_t count(int64_t lo, int64_t hi) const {
+        return on && lo + ty < hi ? static_cast<uint32_t>(hi - lo - ty - 1) / static_cast<uint32_t>(rows) + 1u : 0u;
+    }
+};
+
 // out[k][group] (LDS) = sum over the group of v[k][column] of every thread
-// that is `on`.  sh: [N][ty][slots].  Every thread of the workgroup takes
-// part; `out` is visible to all after the call, and sh may be written again.
-template <int N, int V, bool COL>
-__device__ __forceinline__ void group_sums(const NormArgs& a, const Slots& sl, bool on, int tx, int ty, int nc,
-                                           const float (&v)[N][V], float* sh, float* out) {
-    const int plane = a.ty * sl.n;
-    if (on) {
+// that is `on`.  Every thread of the team takes part; `out` is visible to all
+// after the call, and t.sums may be written again.
+template <int N, int V, bool COL, int SZ>
+__device__ __forceinline__ void group_sums(const NormArgs& a, const Slots& sl, const Team<SZ>& t, int nc,
+                                           const float (&v)[N][V], float* out) {
+    const int plane = t.rows * sl.n;
+    if (t.on) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             if constexpr (COL) {
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    if (e < nc) sh[k * plane + ty * sl.n + tx * V + e] = v[k][e];
+                    if (e < nc) t.sums[k * plane + t.ty * sl.n + t.tx * V + e] = v[k][e];
             } else {
                 float s = v[k][0];
 #pragma unroll
                 for (int e = 1; e < V; ++e) s += v[k][e];
-                sh[k * plane + ty * sl.n + tx] = s;
+                t.sums[k * plane + t.ty * sl.n + t.tx] = s;
             }
         }
     }
-    __syncthreads();
-    // a power of two of lanes to a group, each taking every lpg-th value
-    int lpg = 1;
-    while (lpg < 64 && 2 * lpg * a.groups <= kThreads) lpg *= 2;
-    const int gl = threadIdx.x & (lpg - 1), gpp = kThreads / lpg, vals = a.ty * sl.per_group;
-    const float inv = 1.f / static_cast<float>(sl.per_group);
-    for (int gb = 0; gb < a.groups; gb += gpp) {
-        const int gi = gb + static_cast<int>(threadIdx.x) / lpg;
+    t.sync();
+    // a power of two of lanes to a group: across its slots, and what is left
+    // of them down the rows of threads
+    const int lpg = SZ == 64 ? (a.lanes_per_group > 4 ? a.lanes_per_group / 4 : 1) : a.lanes_per_group;
+    const int lc = a.lanes_per_slots < lpg ? a.lanes_per_slots : lpg;
+    const int shift = __builtin_ctz(lpg), cshift = __builtin_ctz(lc);
+    const int gl = t.tid & (lpg - 1), g0 = t.tid >> shift, c0 = gl & (lc - 1), r0 = gl >> cshift, rs = lpg >> cshift;
+    for (int gb = 0; gb < a.groups; gb += SZ >> shift) {
+        const int gi = gb + g0;
         const bool ok = gi < a.groups;
         float s[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) s[k] = 0.f;
         if (ok) {
-            for (int i = gl; i < vals; i += lpg) {
-                // i = r * per_group + c (below 2^12: the quotient is exact after one step)
-                int r = static_cast<int>(static_cast<float>(i) * inv);
-                int c = i - r * sl.per_group;
-                if (c < 0) { --r; c += sl.per_group; }
-                if (c >= sl.per_group) { ++r; c -= sl.per_group; }
+            const float* p = t.sums + r0 * sl.n + gi * sl.per_group;
+            for (int r = r0; r < t.rows; r += rs, p += rs * sl.n)
+                for (int c = c0; c < sl.per_group; c += lc)
 #pragma unroll
-                for (int k = 0; k < N; ++k) s[k] += sh[k * plane + r * sl.n + gi * sl.per_group + c];
-            }
+                    for (int k = 0; k < N; ++k) s[k] += p[k * plane + c];
         }
         for (int o = 1; o < lpg; o *= 2)
 #pragma unroll
@@ -231,7 +263,7 @@ __device__ __forceinline__ void group_sums(const NormArgs& a, const Slots& sl, b
 #pragma unroll
             for (int k = 0; k < N; ++k) out[k * a.groups + gi] = s[k];
     }
-    __syncthreads();
+    t.sync();
 }
 
 // This thread's columns: the affine and, per graph, the statistics (one of
@@ -248,7 +280,7 @@ struct Cols {
             const int c = c0 + e < a.d ? c0 + e : static_cast<int>(a.d) - 1;
             w[e] = a.w ? a.w[c] : 1.f;
             v[e] = a.v ? a.v[c] : 0.f;
-            if (e < G) grp[e] = c / a.gd;
+            if (e < G) grp[e] = static_cast<int>(static_cast<uint32_t>(c) / static_cast<uint32_t>(a.gd));
         }
     }
     __device__ __forceinline__ void graph(const NormArgs& a, int64_t g) {
@@ -271,112 +303,218 @@ __device__ __forceinline__ void norm_store(T* p, u32x4_t q, const Cols<Vec<T>::N
     store_first<T>(p, f, nc);
 }
 
-// The first `cnt` of the thread's rows from x on: Out from X.
+// The thread's rows of lo .. hi - 1: Out from X.
 template <class T, int ACT, bool COL>
-__device__ __forceinline__ void apply_rows(const T* x, int64_t sx, T* out, int64_t so, int64_t cnt,
-                                           const Cols<Vec<T>::N, COL>& k, const float (&rw)[Vec<T>::N], float slope,
-                                           int nc) {
-    char* po = reinterpret_cast<char*>(out);
-    each_row<false>(x, sx, nullptr, 0, cnt, [&](u32x4_t q, u32x4_t) {
-        norm_store<T, ACT, COL>(reinterpret_cast<T*>(po), q, k, rw, slope, nc);
-        po += so;
+__device__ __forceinline__ void apply_rows(const NormArgs& a, const Team<kThreads>& t, int64_t lo, int64_t hi,
+                                           const Cols<Vec<T>::N, COL>& k, const float (&rw)[Vec<T>::N], int nc) {
+    constexpr int64_t ES = sizeof(T);
+    const uint32_t cnt = t.count(lo, hi);
+    if (!cnt) return;
+    const int64_t r = lo + t.ty, c0 = t.tx * Vec<T>::N;
+    char* po = reinterpret_cast<char*>(static_cast<T*>(a.out) + r * a.ldo + c0);
+    each_row<false>(static_cast<const T*>(a.x) + r * a.ldx + c0, t.rows * a.ldx * ES, nullptr, 0, cnt, [&](u32x4_t q, u32x4_t) {
+        norm_store<T, ACT, COL>(reinterpret_cast<T*>(po), q, k, rw, a.slope, nc);
+        po += t.rows * a.ldo * ES;
     });
 }
 
 // ---- forward ----------------------------------------------------------------------------
-// First pass: workgroups below graph_blocks do short graphs whole (and give
-// graphs without rows their statistics), the others take the chunks' pieces
-// of long graphs: mean and squares about it.
+// mean and rstd of graph g out of the groups' sums and squares in t.gs, and
+// the thread's rstd w.
+template <int V, bool COL, int SZ>
+__device__ __forceinline__ void put_stats(const NormArgs& a, const Team<SZ>& t, Cols<V, COL>& k, int64_t g, float itot,
+                                          float (&rw)[V]) {
+    const float* gsq = t.gs + a.groups;
+    for (int i = t.tid; i < a.groups; i += SZ) {
+        a.mean[g * a.groups + i] = t.gs[i] * itot;
+        a.rstd[g * a.groups + i] = __builtin_amdgcn_rsqf(gsq[i] * itot + a.eps);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (e < k.G) k.rstd[e] = __builtin_amdgcn_rsqf(gsq[k.grp[e]] * itot + a.eps);
+        rw[e] = k.rstd[k.of(e)] * k.w[e];
+    }
+}
+
+// The group means of rows lo .. hi - 1 (k.mean; times the count in t.gs) and
+// squares about them (t.gs + groups); returns 1 / the count.
+template <class T, bool COL>
+__device__ __forceinline__ float norm_stats(const NormArgs& a, const Slots& sl, const Team<kThreads>& t,
+                                            Cols<Vec<T>::N, COL>& k, int nc, int64_t lo, int64_t hi) {
+    constexpr int V = Vec<T>::N;
+    const uint32_t cnt = t.count(lo, hi);
+    const float n = static_cast<float>(cnt);
+    float m[V], s[V], c[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = s[e] = c[e] = 0.f;
+    if (cnt) {
+        const T* x = static_cast<const T*>(a.x) + (lo + t.ty) * a.ldx + t.tx * V;
+        unpack_vec<T>(load16(x), c);
+        each_row<false>(x, t.rows * a.ldx * static_cast<int64_t>(sizeof(T)), nullptr, 0, cnt, [&](u32x4_t q, u32x4_t) {
+            float f[V];
+            unpack_vec<T>(q, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float u = f[e] - c[e];
+                m[e] += u;
+                s[e] = fmaf(u, u, s[e]);
+            }
+        });
+        const float inv = 1.f / n;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float u = m[e] * inv;
+            s[e] = fmaxf(fmaf(-u, m[e], s[e]), 0.f);
+            m[e] = c[e] + u;
+        }
+    }
+    const float itot = 1.f / (static_cast<float>(hi - lo) * static_cast<float>(a.gd));
+    float v[1][V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[0][e] = e < nc ? m[e] * n : 0.f;
+    group_sums<1, V, COL>(a, sl, t, nc, v, t.gs);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (e < k.G) k.mean[e] = t.gs[k.grp[e]] * itot;
+        const float dm = m[e] - k.mean[k.of(e)];
+        v[0][e] = e < nc ? fmaf(dm * dm, n, s[e]) : 0.f;
+    }
+    group_sums<1, V, COL>(a, sl, t, nc, v, t.gs + a.groups);
+    // (t.gs stays until the next call's first barrier)
+    return itot;
+}
+
+// Graph g of at most kWaveHold rows a thread, whole, by one wavefront that
+// keeps the rows in registers: read once, summed, summed about the mean,
+// written.
 template <class T, int ACT, bool COL>
-__global__ __launch_bounds__(kThreads, 4) void norm_first(NormArgs a) {
+__device__ __forceinline__ void norm_held(const NormArgs& a, const Slots& sl, const Team<64>& t, Cols<Vec<T>::N, COL>& k,
+                                          int nc, int64_t g, int64_t lo, int64_t hi) {
+    constexpr int V = Vec<T>::N, B = 4;
+    const int cnt = static_cast<int>(t.count(lo, hi));
+    const int steps = static_cast<int>((static_cast<uint32_t>(hi - lo) + t.rows - 1) / static_cast<uint32_t>(t.rows));   // of all lanes
+    const int64_t sx = t.rows * a.ldx * static_cast<int64_t>(sizeof(T)), so = t.rows * a.ldo * static_cast<int64_t>(sizeof(T));
+    const char* px = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + (cnt ? lo + t.ty : lo) * a.ldx + t.tx * V);
+    u32x4_t q[kWaveHold];
+#pragma unroll
+    for (int b = 0; b < kWaveHold; b += B)
+        if (b < steps) {
+#pragma unroll
+            for (int i = b; i < b + B; ++i) {
+                q[i] = load16(px);
+                if (i + 1 < cnt) px += sx;
+            }
+        }
+    float v[1][V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[0][e] = 0.f;
+    // (a row past the thread's last is its last again, with weight 0)
+#pragma unroll
+    for (int b = 0; b < kWaveHold; b += B)
+        if (b < steps) {
+#pragma unroll
+            for (int i = b; i < b + B; ++i) {
+                const float mk = i < cnt ? 1.f : 0.f;
+                float f[V];
+                unpack_vec<T>(q[i], f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[0][e] = fmaf(f[e], mk, v[0][e]);
+            }
+        }
+    const float itot = 1.f / (static_cast<float>(hi - lo) * static_cast<float>(a.gd));
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[0][e] = e < nc ? v[0][e] : 0.f;
+    group_sums<1, V, COL>(a, sl, t, nc, v, t.gs);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (e < k.G) k.mean[e] = t.gs[k.grp[e]] * itot;
+        v[0][e] = 0.f;
+    }
+    // (unpacked again: in fp32 the rows would take twice their registers)
+#pragma unroll
+    for (int i = 0; i < kWaveHold; ++i) asm volatile("" : "+v"(q[i]));
+#pragma unroll
+    for (int b = 0; b < kWaveHold; b += B)
+        if (b < steps) {
+#pragma unroll
+            for (int i = b; i < b + B; ++i) {
+                const float mk = i < cnt ? 1.f : 0.f;
+                float f[V];
+                unpack_vec<T>(q[i], f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float u = f[e] - k.mean[k.of(e)];
+                    v[0][e] = fmaf(u * mk, u, v[0][e]);
+                }
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[0][e] = e < nc ? v[0][e] : 0.f;
+    group_sums<1, V, COL>(a, sl, t, nc, v, t.gs + a.groups);
+    float rw[V];
+    put_stats(a, t, k, g, itot, rw);
+#pragma unroll
+    for (int i = 0; i < kWaveHold; ++i) asm volatile("" : "+v"(q[i]));
+    char* po = reinterpret_cast<char*>(static_cast<T*>(a.out) + (cnt ? lo + t.ty : lo) * a.ldo + t.tx * V);
+#pragma unroll
+    for (int i = 0; i < kWaveHold; ++i)
+        if (i < cnt) {
+            norm_store<T, ACT, COL>(reinterpret_cast<T*>(po), q[i], k, rw, a.slope, nc);
+            po += so;
+        }
+}
+
+// First pass, three kinds of workgroups in one launch: the first graph_blocks
+// take short graphs one at a time (and give graphs without rows their
+// statistics), the next wave_blocks the shortest ones, four at a time, and the
+// rest the chunks' pieces of long graphs: mean and squares about it.  (With
+// the wavefronts' graphs first all of them start at once and wait for memory
+// and compute together: 54 us for 4096 graphs of 25 rows of 256 bf16, 45 in
+// this order.)
+template <class T, int ACT, bool COL>
+__global__ __launch_bounds__(kThreads, COL ? 3 : 4) void norm_first(NormArgs a) {
     constexpr int V = Vec<T>::N;
     extern __shared__ __attribute__((aligned(16))) float sh[];
     const Slots sl = slots_of<COL>(a.d, a.gd, a.tx, V);
-    float* gsum = sh + a.ty * sl.n;       // [groups]
-    float* gsq = gsum + a.groups;         // [groups]
-    const int tx = threadIdx.x % a.tx, ty = threadIdx.x / a.tx;
-    const bool on = ty < a.ty;
-    const int c0 = tx * V;
-    const int nc = a.d - c0 < V ? static_cast<int>(a.d) - c0 : V;
-    const T* x = static_cast<const T*>(a.x) + c0;
-    T* out = static_cast<T*>(a.out) + c0;
+    const int d = static_cast<int>(a.d);
     Cols<V, COL> k;
-    k.init(a, c0);
-    const int64_t sx = a.ty * a.ldx * static_cast<int64_t>(sizeof(T)), so = a.ty * a.ldo * static_cast<int64_t>(sizeof(T));
-    // the group means (k.mean, and gsum / total) and squares about them (gsq) of rows lo .. hi - 1
-    auto stats = [&](int64_t lo, int64_t hi) {
-        const uint32_t cnt = on ? rows_of(a, lo + ty, hi) : 0u;
-        const float n = static_cast<float>(cnt);
-        float m[V], s[V], c[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) m[e] = s[e] = c[e] = 0.f;
-        if (cnt) {
-            const T* xr = x + (lo + ty) * a.ldx;
-            unpack_vec<T>(load16(xr), c);
-            each_row<false>(xr, sx, nullptr, 0, cnt, [&](u32x4_t q, u32x4_t) {
-                float f[V];
-                unpack_vec<T>(q, f);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float t = f[e] - c[e];
-                    m[e] += t;
-                    s[e] = fmaf(t, t, s[e]);
-                }
-            });
-            const float inv = 1.f / n;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float t = m[e] * inv;
-                s[e] = fmaxf(fmaf(-t, m[e], s[e]), 0.f);
-                m[e] = c[e] + t;
-            }
+    if (blockIdx.x >= a.graph_blocks && blockIdx.x < a.graph_blocks + a.wave_blocks) {
+        const Team<64> t(a, sl, 1, sh);
+        k.init(a, t.tx * V);
+        for (int64_t g = 4 * (static_cast<int64_t>(blockIdx.x) - a.graph_blocks) + (threadIdx.x >> 6); g < a.n_seg; g += 4 * a.wave_blocks) {
+            const int64_t lo = seg_at(a, g), hi = seg_at(a, g + 1);
+            if (lo < hi && hi - lo <= a.wave_rows) norm_held<T, ACT, COL>(a, sl, t, k, d - t.tx * V, g, lo, hi);
         }
-        const float itot = 1.f / (static_cast<float>(hi - lo) * static_cast<float>(a.gd));
-        float v[1][V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[0][e] = e < nc ? m[e] * n : 0.f;
-        group_sums<1, V, COL>(a, sl, on, tx, ty, nc, v, sh, gsum);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            if (e < k.G) k.mean[e] = gsum[k.grp[e]] * itot;
-            const float dm = m[e] - k.mean[k.of(e)];
-            v[0][e] = e < nc ? s[e] + dm * dm * n : 0.f;
-        }
-        group_sums<1, V, COL>(a, sl, on, tx, ty, nc, v, sh, gsq);
-        // (gsum and gsq stay until the next call's first barrier)
-        return itot;
-    };
+        return;
+    }
+    const Team<kThreads> t(a, sl, 1, sh);
+    const int nc = d - t.tx * V;
+    bool ready = false;
     if (blockIdx.x < a.graph_blocks) {
         for (int64_t g = blockIdx.x; g < a.n_seg; g += a.graph_blocks) {
             const int64_t lo = seg_at(a, g), hi = seg_at(a, g + 1);
-            if (hi - lo > a.short_rows) continue;
             if (hi <= lo) {
                 for (int i = threadIdx.x; i < a.groups; i += kThreads) {
                     a.mean[g * a.groups + i] = 0.f;
                     a.rstd[g * a.groups + i] = 1.f / sqrtf(a.eps);
                 }
-                continue;
             }
-            const float itot = stats(lo, hi);
-            for (int i = threadIdx.x; i < a.groups; i += kThreads) {
-                a.mean[g * a.groups + i] = gsum[i] * itot;
-                a.rstd[g * a.groups + i] = __builtin_amdgcn_rsqf(gsq[i] * itot + a.eps);
-            }
+            if (hi - lo <= (a.wave_blocks ? a.wave_rows : 0) || hi - lo > a.short_rows) continue;
+            if (!ready) k.init(a, t.tx * V);
+            ready = true;
+            const float itot = norm_stats<T, COL>(a, sl, t, k, nc, lo, hi);
             float rw[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (e < k.G) k.rstd[e] = __builtin_amdgcn_rsqf(gsq[k.grp[e]] * itot + a.eps);
-                rw[e] = k.rstd[k.of(e)] * k.w[e];
-            }
+            put_stats(a, t, k, g, itot, rw);
             // (every row is read before it is written, by the same thread)
-            apply_rows<T, ACT, COL>(x + (lo + ty) * a.ldx, sx, out + (lo + ty) * a.ldo, so,
-                                    on ? rows_of(a, lo + ty, hi) : 0u, k, rw, a.slope, nc);
+            apply_rows<T, ACT, COL>(a, t, lo, hi, k, rw, nc);
         }
     } else {
-        for_pieces(a, static_cast<int64_t>(blockIdx.x) - a.graph_blocks, [&](int64_t, int64_t lo, int64_t hi, int64_t piece) {
-            const float itot = stats(lo, hi);
+        for_pieces(a, static_cast<int64_t>(blockIdx.x) - a.graph_blocks - a.wave_blocks, [&](int64_t, int64_t lo, int64_t hi, int64_t piece) {
+            if (!ready) k.init(a, t.tx * V);
+            ready = true;
+            const float itot = norm_stats<T, COL>(a, sl, t, k, nc, lo, hi);
             for (int i = threadIdx.x; i < a.groups; i += kThreads)
-                a.piece[piece * a.groups + i] = make_float2(gsum[i] * itot, gsq[i]);
+                a.piece[piece * a.groups + i] = make_float2(t.gs[i] * itot, t.gs[a.groups + i]);
         });
     }
 }
@@ -452,26 +590,18 @@ __global__ __launch_bounds__(kThreads) void norm_join(NormArgs a) {
 template <class T, int ACT, bool COL>
 __global__ __launch_bounds__(kThreads, 4) void norm_apply(NormArgs a) {
     constexpr int V = Vec<T>::N;
-    const int tx = threadIdx.x % a.tx;
-    // (a thread past the last row of threads walks along with no rows: the
-    // search for a row's graph takes whole wavefronts)
-    const int ty = threadIdx.x / a.tx;
-    const bool on = ty < a.ty;
-    const int c0 = tx * V;
-    const int nc = a.d - c0 < V ? static_cast<int>(a.d) - c0 : V;
-    const T* x = static_cast<const T*>(a.x) + c0;
-    T* out = static_cast<T*>(a.out) + c0;
+    const Team<kThreads> t(a, Slots{0, 0}, 0, nullptr);
     Cols<V, COL> k;
-    k.init(a, c0);
+    bool ready = false;
     // the last chunks first: they are what the first pass left in the caches
     for_pieces(a, a.n_chunks - 1 - static_cast<int64_t>(blockIdx.x), [&](int64_t g, int64_t lo, int64_t hi, int64_t) {
+        if (!ready) k.init(a, t.tx * V);
+        ready = true;
         k.graph(a, g);
         float rw[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) rw[e] = k.rstd[k.of(e)] * k.w[e];
-        if (!on || lo + ty >= hi) return;
-        apply_rows<T, ACT, COL>(x + (lo + ty) * a.ldx, a.ty * a.ldx * static_cast<int64_t>(sizeof(T)), out + (lo + ty) * a.ldo,
-                                a.ty * a.ldo * static_cast<int64_t>(sizeof(T)), rows_of(a, lo + ty, hi), k, rw, a.slope, nc);
+        apply_rows<T, ACT, COL>(a, t, lo, hi, k, rw, static_cast<int>(a.d) - t.tx * V);
     });
 }
 
@@ -522,104 +652,109 @@ __device__ __forceinline__ void norm_dx_store(T* p, u32x4_t qx, u32x4_t qg, cons
     store_first<T>(p, f, nc);
 }
 
-// The thread's rows lo + ty, lo + 2 ty, ... below hi: dX.
+// The thread's rows of lo .. hi - 1: dX.
 template <class T, int ACT, bool COL>
-__device__ __forceinline__ void dx_rows(const NormArgs& a, int c0, int64_t r, int64_t hi,
+__device__ __forceinline__ void dx_rows(const NormArgs& a, const Team<kThreads>& t, int64_t lo, int64_t hi,
                                         const Cols<Vec<T>::N, COL>& k, const float (&m0)[Cols<Vec<T>::N, COL>::G],
                                         const float (&m1)[Cols<Vec<T>::N, COL>::G], int nc) {
     constexpr int64_t ES = sizeof(T);
+    const uint32_t cnt = t.count(lo, hi);
+    if (!cnt) return;
+    const int64_t r = lo + t.ty, c0 = t.tx * Vec<T>::N;
     char* po = reinterpret_cast<char*>(static_cast<T*>(a.out) + r * a.ldo + c0);
-    each_row<true>(static_cast<const T*>(a.x) + r * a.ldx + c0, a.ty * a.ldx * ES,
-                   static_cast<const T*>(a.g) + r * a.ldg + c0, a.ty * a.ldg * ES, rows_of(a, r, hi),
-                   [&](u32x4_t qx, u32x4_t qg) {
+    each_row<true>(static_cast<const T*>(a.x) + r * a.ldx + c0, t.rows * a.ldx * ES,
+                   static_cast<const T*>(a.g) + r * a.ldg + c0, t.rows * a.ldg * ES, cnt, [&](u32x4_t qx, u32x4_t qg) {
                        norm_dx_store<T, ACT, COL>(reinterpret_cast<T*>(po), qx, qg, k, m0, m1, a.slope, nc);
-                       po += a.ty * a.ldo * ES;
+                       po += t.rows * a.ldo * ES;
                    });
 }
 
+// Rows lo .. hi - 1 of graph g: the column sums of a and a xhat added to the
+// thread's place of acc ([2][a.ty][d]), the groups' sums
+// of h and h xhat (t.gs) and, for a whole graph (piece -1), dX.
+template <class T, int ACT, bool COL>
+__device__ __forceinline__ void norm_bwd_part(const NormArgs& a, const Slots& sl, const Team<kThreads>& t,
+                                              Cols<Vec<T>::N, COL>& k, float* acc, int64_t g, int64_t lo,
+                                              int64_t hi, int64_t piece) {
+    constexpr int V = Vec<T>::N;
+    constexpr int64_t ES = sizeof(T);
+    const int d = static_cast<int>(a.d), c0 = t.tx * V, nc = d - c0;
+    k.graph(a, g);
+    float t0[V], t1[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) t0[e] = t1[e] = 0.f;
+    const uint32_t cnt = t.count(lo, hi);
+    if (cnt) {
+        const int64_t r = lo + t.ty;
+        each_row<true>(static_cast<const T*>(a.x) + r * a.ldx + c0, t.rows * a.ldx * ES,
+                       static_cast<const T*>(a.g) + r * a.ldg + c0, t.rows * a.ldg * ES, cnt, [&](u32x4_t qx, u32x4_t qg) {
+                           float f[V], q[V];
+                           unpack_vec<T>(qx, f);
+                           unpack_vec<T>(qg, q);
+#pragma unroll
+                           for (int e = 0; e < V; ++e) {
+                               float xh;
+                               const int j = k.of(e);
+                               const float u = grad_a<ACT>(f[e], q[e], k.mean[j], k.rstd[j], Affine<ACT>(k.rstd[j], k.w[e]),
+                                                           k.v[e], a.slope, xh);
+                               t0[e] += u;
+                               t1[e] = fmaf(u, xh, t1[e]);
+                           }
+                       });
+        float* p = acc + t.ty * d + c0;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < nc) {
+                p[e] += t0[e];
+                p[a.ty * d + e] += t1[e];
+            }
+    }
+    if (!a.out) return;
+    float v[2][V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        v[0][e] = e < nc ? t0[e] * k.w[e] : 0.f;
+        v[1][e] = e < nc ? t1[e] * k.w[e] : 0.f;
+    }
+    group_sums<2, V, COL>(a, sl, t, nc, v, t.gs);
+    if (piece >= 0) {
+        for (int i = t.tid; i < a.groups; i += kThreads) a.piece[piece * a.groups + i] = make_float2(t.gs[i], t.gs[a.groups + i]);
+    } else {
+        const float inv = 1.f / (static_cast<float>(hi - lo) * static_cast<float>(a.gd));
+        float m0[Cols<V, COL>::G], m1[Cols<V, COL>::G];
+#pragma unroll
+        for (int e = 0; e < Cols<V, COL>::G; ++e) {
+            m0[e] = t.gs[k.grp[e]] * inv;
+            m1[e] = t.gs[a.groups + k.grp[e]] * inv;
+        }
+        dx_rows<T, ACT, COL>(a, t, lo, hi, k, m0, m1, nc);
+    }
+}
+
 // First pass: dX of short graphs whole (when wanted), the pieces' sums of h
-// and h xhat of long ones, and each workgroup's column sums of a and a xhat.
+// and h xhat of long ones, and each workgroup's column sums of a and a xhat;
+// workgroups as in the forward pass.
 template <class T, int ACT, bool COL>
 __global__ __launch_bounds__(kThreads, COL ? 2 : 3) void norm_bwd_first(NormArgs a) {
     constexpr int V = Vec<T>::N;
     extern __shared__ __attribute__((aligned(16))) float sh[];
     const Slots sl = slots_of<COL>(a.d, a.gd, a.tx, V);
     const int d = static_cast<int>(a.d);
-    float* acc = sh + 2 * a.ty * sl.n;    // [2][ty][d]: the sums of a and a xhat, each thread its own
-    float* gsum = acc + 2 * a.ty * d;     // [2][groups]
-    const int tx = threadIdx.x % a.tx, ty = threadIdx.x / a.tx;
-    const bool on = ty < a.ty;
-    const int c0 = tx * V;
-    const int nc = d - c0 < V ? d - c0 : V;
-    const T* x = static_cast<const T*>(a.x) + c0;
-    const T* gr = static_cast<const T*>(a.g) + c0;
-    T* out = static_cast<T*>(a.out) + c0;
+    float* acc = sh + 2 * a.ty * sl.n + stat_floats(a);
+    for (int i = threadIdx.x; i < 2 * a.ty * d; i += kThreads) acc[i] = 0.f;
+    __syncthreads();
     Cols<V, COL> k;
-    k.init(a, c0);
-    float* acc0 = acc + ty * d + c0;
-    float* acc1 = acc0 + a.ty * d;
-    if (on)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (e < nc) acc0[e] = acc1[e] = 0.f;
-    // (piece -1: the whole of a short graph)
-    auto part = [&](int64_t g, int64_t lo, int64_t hi, int64_t piece) {
-        k.graph(a, g);
-        float t0[V], t1[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) t0[e] = t1[e] = 0.f;
-        if (on && lo + ty < hi)
-            each_row<true>(x + (lo + ty) * a.ldx, a.ty * a.ldx * static_cast<int64_t>(sizeof(T)), gr + (lo + ty) * a.ldg,
-                           a.ty * a.ldg * static_cast<int64_t>(sizeof(T)), rows_of(a, lo + ty, hi), [&](u32x4_t qx, u32x4_t qg) {
-                float f[V], q[V];
-                unpack_vec<T>(qx, f);
-                unpack_vec<T>(qg, q);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float xh;
-                    const int j = k.of(e);
-                    const float t = grad_a<ACT>(f[e], q[e], k.mean[j], k.rstd[j], Affine<ACT>(k.rstd[j], k.w[e]), k.v[e],
-                                                a.slope, xh);
-                    t0[e] += t;
-                    t1[e] = fmaf(t, xh, t1[e]);
-                }
-            });
-        if (on)
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (e < nc) {
-                    acc0[e] += t0[e];
-                    acc1[e] += t1[e];
-                }
-        if (!a.out) return;
-        float v[2][V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            v[0][e] = e < nc ? t0[e] * k.w[e] : 0.f;
-            v[1][e] = e < nc ? t1[e] * k.w[e] : 0.f;
-        }
-        group_sums<2, V, COL>(a, sl, on, tx, ty, nc, v, sh, gsum);
-        if (piece >= 0) {
-            for (int i = threadIdx.x; i < a.groups; i += kThreads)
-                a.piece[piece * a.groups + i] = make_float2(gsum[i], gsum[a.groups + i]);
-        } else {
-            const float inv = 1.f / (static_cast<float>(hi - lo) * static_cast<float>(a.gd));
-            float m0[k.G], m1[k.G];
-#pragma unroll
-            for (int e = 0; e < k.G; ++e) {
-                m0[e] = gsum[k.grp[e]] * inv;
-                m1[e] = gsum[a.groups + k.grp[e]] * inv;
-            }
-            if (on && lo + ty < hi) dx_rows<T, ACT, COL>(a, c0, lo + ty, hi, k, m0, m1, nc);
-        }
-    };
+    const Team<kThreads> t(a, sl, 2, sh);
+    k.init(a, t.tx * V);
     if (blockIdx.x < a.graph_blocks) {
         for (int64_t g = blockIdx.x; g < a.n_seg; g += a.graph_blocks) {
             const int64_t lo = seg_at(a, g), hi = seg_at(a, g + 1);
-            if (lo < hi && hi - lo <= a.short_rows) part(g, lo, hi, -1);
+            if (lo < hi && hi - lo <= a.short_rows) norm_bwd_part<T, ACT, COL>(a, sl, t, k, acc, g, lo, hi, -1);
         }
     } else {
-        for_pieces(a, static_cast<int64_t>(blockIdx.x) - a.graph_blocks, part);
+        for_pieces(a, static_cast<int64_t>(blockIdx.x) - a.graph_blocks, [&](int64_t g, int64_t lo, int64_t hi, int64_t piece) {
+            norm_bwd_part<T, ACT, COL>(a, sl, t, k, acc, g, lo, hi, piece);
+        });
     }
     if (a.col) {
         // the thread rows of each column, in order
@@ -662,37 +797,31 @@ __global__ __launch_bounds__(kColThreads) void norm_cols(const float* __restrict
 template <class T, int ACT, bool COL>
 __global__ __launch_bounds__(kThreads, COL ? 2 : 3) void norm_bwd_apply(NormArgs a) {
     constexpr int V = Vec<T>::N;
-    const int tx = threadIdx.x % a.tx;
-    const int ty = threadIdx.x / a.tx;
-    const bool on = ty < a.ty;
-    const int c0 = tx * V;
-    const int nc = a.d - c0 < V ? static_cast<int>(a.d) - c0 : V;
-    const T* x = static_cast<const T*>(a.x) + c0;
-    const T* gr = static_cast<const T*>(a.g) + c0;
-    T* out = static_cast<T*>(a.out) + c0;
+    const Team<kThreads> t(a, Slots{0, 0}, 0, nullptr);
     Cols<V, COL> k;
-    k.init(a, c0);
+    k.init(a, t.tx * V);
     for_pieces(a, a.n_chunks - 1 - static_cast<int64_t>(blockIdx.x), [&](int64_t g, int64_t lo, int64_t hi, int64_t) {
         k.graph(a, g);
-        float m0[k.G], m1[k.G];
+        float m0[Cols<V, COL>::G], m1[Cols<V, COL>::G];
 #pragma unroll
-        for (int e = 0; e < k.G; ++e) {
+        for (int e = 0; e < Cols<V, COL>::G; ++e) {
             const float2 q = a.stat[g * a.groups + k.grp[e]];
             m0[e] = q.x;
             m1[e] = q.y;
         }
-        if (on && lo + ty < hi) dx_rows<T, ACT, COL>(a, c0, lo + ty, hi, k, m0, m1, nc);
+        dx_rows<T, ACT, COL>(a, t, lo, hi, k, m0, m1, static_cast<int>(a.d) - t.tx * V);
     });
 }
 
 struct Plan {
     int tx, ty;
     int64_t rows_per_chunk, n_chunks, short_rows;
-    int64_t graph_blocks, chunk_blocks;   // of the first pass
+    int64_t wave_rows, graph_blocks, wave_blocks, chunk_blocks;   // of the first pass
+    int64_t blocks() const { return graph_blocks + wave_blocks + chunk_blocks; }
 };
 
 // At most kMaxChunks chunks, of at least half a short graph.
-Plan norm_plan(int64_t n_rows, int64_t d, int64_t n_seg, bool one, sag_dtype dt) {
+Plan norm_plan(int64_t n_rows, int64_t d, int64_t n_seg, bool one, bool bwd, sag_dtype dt) {
     Plan p;
     p.tx = static_cast<int>(cdiv(d, vec_elems(dt)));
     p.ty = kThreads / p.tx;
@@ -705,7 +834,17 @@ Plan norm_plan(int64_t n_rows, int64_t d, int64_t n_seg, bool one, sag_dtype dt)
     // graph of all rows
     const bool all_short = n_rows <= p.short_rows;
     p.chunk_blocks = all_short || n_seg == 0 ? 0 : p.n_chunks;
-    p.graph_blocks = one && !all_short ? 0 : (n_seg < kMaxGraphBlocks ? n_seg : kMaxGraphBlocks);
+    const bool graphs = !(one && !all_short);
+    p.graph_blocks = graphs ? (n_seg < kMaxGraphBlocks ? n_seg : kMaxGraphBlocks) : 0;
+    // a wavefront has two rows of threads or more there: wider rows would
+    // leave up to half its lanes without a column.  A batch of few graphs
+    // has workgroups to spare (25 rows of 256 bf16, 8 groups, workgroups ->
+    // wavefronts: 256 graphs 16.7 -> 17.8 us, 512 20.3 -> 19.4, 4096 64 ->
+    // 52; graphs of 100 rows, all past wave_rows, lose 2%: 154 -> 157).  The
+    // backward pass, of two inputs, was no faster so (57 us for 1200 graphs
+    // of 25 rows of 100 fp32, 54 by workgroups).
+    p.wave_rows = p.tx <= 32 ? kWaveHold * static_cast<int64_t>(64 / p.tx) : 0;
+    p.wave_blocks = !bwd && graphs && p.wave_rows && n_seg >= kManyGraphs ? (n_seg < 4 * kMaxGraphBlocks ? cdiv(n_seg, 4) : kMaxGraphBlocks) : 0;
     return p;
 }
 
@@ -715,6 +854,14 @@ dim3 join_grid(NormArgs& a) {
     a.seg_per_block = cdiv(a.n_seg, 2048);
     a.grp_per_block = a.n_seg < 256 && a.groups > 2 ? 2 : a.groups;
     return dim3(static_cast<unsigned>(cdiv(a.n_seg, a.seg_per_block)), static_cast<unsigned>(cdiv(a.groups, a.grp_per_block)));
+}
+
+// Lanes that add up a group's slots: what gives every group some at once, as
+// many of them across the slots as a row of threads has.
+void set_group_lanes(NormArgs& a, int per_group) {
+    a.lanes_per_group = a.lanes_per_slots = 1;
+    while (a.lanes_per_group < 64 && 2 * a.lanes_per_group * a.groups <= kThreads) a.lanes_per_group *= 2;
+    while (a.lanes_per_slots < per_group && a.lanes_per_slots < 64) a.lanes_per_slots *= 2;
 }
 
 template <class F>
@@ -736,7 +883,7 @@ Ws norm_ws(const Plan& p, int64_t d, int64_t n_seg, int64_t groups, bool bwd, vo
     w.piece = c.take<float2>((p.n_chunks + n_seg) * groups);
     if (bwd) {
         w.stat = c.take<float2>(n_seg * groups);
-        w.col = c.take<float>((p.graph_blocks + p.chunk_blocks) * 2 * d);
+        w.col = c.take<float>(p.blocks() * 2 * d);
     }
     w.used = c.used();
     w.fits = c.fits();
@@ -764,7 +911,7 @@ using namespace sag;
 extern "C" size_t sag_group_norm_forward_workspace_bytes(int64_t n_rows, int64_t d, int64_t groups, int64_t n_seg,
                                                          sag_dtype dt) {
     if (n_rows < 0 || d < 1 || groups < 1 || n_seg < 0 || (dt != SAG_F32 && dt != SAG_BF16) || d > 256 * vec_elems(dt)) return 0;
-    return norm_ws(norm_plan(n_rows, d, n_seg, false, dt), d, n_seg, groups, false, nullptr, 0).used;
+    return norm_ws(norm_plan(n_rows, d, n_seg, false, false, dt), d, n_seg, groups, false, nullptr, 0).used;
 }
 
 extern "C" sag_status sag_group_norm_forward(const void* X, int64_t ldx, int64_t n_rows, int64_t d, int64_t groups,
@@ -778,7 +925,7 @@ extern "C" sag_status sag_group_norm_forward(const void* X, int64_t ldx, int64_t
     SAG_TRY(check_dense("group_norm Out", Out, n_rows, d, ldo, dt));
     if (n_seg == 0) return SAG_OK;
     if (!mean || !rstd) return fail(SAG_E_INVALID, who + ": null mean or rstd");
-    const Plan p = norm_plan(n_rows, d, n_seg, !seg, dt);
+    const Plan p = norm_plan(n_rows, d, n_seg, !seg, false, dt);
     const Ws q = norm_ws(p, d, n_seg, groups, false, ws, ws_bytes);
     if (!ws || !aligned16(ws) || !q.fits) return fail(SAG_E_WORKSPACE, who + ": workspace too small");
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -789,8 +936,8 @@ extern "C" sag_status sag_group_norm_forward(const void* X, int64_t ldx, int64_t
     a.groups = static_cast<int>(groups); a.gd = static_cast<int>(d / groups);
     a.seg = seg; a.n_seg = n_seg; a.w = w; a.v = b; a.eps = eps; a.slope = slope;
     a.mean = mean; a.rstd = rstd; a.out = Out; a.ldo = ldo;
-    a.piece = q.piece; a.rows_per_chunk = p.rows_per_chunk; a.n_chunks = p.n_chunks; a.short_rows = p.short_rows; a.graph_blocks = p.graph_blocks; a.tx = p.tx; a.ty = p.ty;
-    const unsigned first = static_cast<unsigned>(p.graph_blocks + p.chunk_blocks);
+    a.piece = q.piece; a.rows_per_chunk = p.rows_per_chunk; a.n_chunks = p.n_chunks; a.short_rows = p.short_rows; a.wave_rows = p.wave_rows; a.graph_blocks = p.graph_blocks; a.wave_blocks = p.wave_blocks; a.tx = p.tx; a.ty = p.ty;
+    const unsigned first = static_cast<unsigned>(p.blocks());
     const unsigned nc = static_cast<unsigned>(p.chunk_blocks);
     const dim3 jgrid = join_grid(a);
     with_act(act, [&](auto ac) {
@@ -799,7 +946,8 @@ extern "C" sag_status sag_group_norm_forward(const void* X, int64_t ldx, int64_t
             using T = decltype(tag);
             by_column(a.gd % Vec<T>::N != 0, [&](auto cc) {
                 constexpr bool COL = decltype(cc)::value;
-                const size_t lds = (static_cast<size_t>(p.ty) * slots_of<COL>(d, a.gd, p.tx, Vec<T>::N).n + 2 * groups) * 4;
+                const size_t lds = (static_cast<size_t>(p.ty) * slots_of<COL>(d, a.gd, p.tx, Vec<T>::N).n + stat_floats(a)) * 4;
+                set_group_lanes(a, slots_of<COL>(d, a.gd, p.tx, Vec<T>::N).per_group);
                 norm_first<T, ACT, COL><<<first, kThreads, lds, s>>>(a);
             });
             if (!nc) return;
@@ -817,7 +965,7 @@ extern "C" sag_status sag_group_norm_forward(const void* X, int64_t ldx, int64_t
 extern "C" size_t sag_group_norm_backward_workspace_bytes(int64_t n_rows, int64_t d, int64_t groups, int64_t n_seg,
                                                           sag_dtype dt) {
     if (n_rows < 0 || d < 1 || groups < 1 || n_seg < 0 || (dt != SAG_F32 && dt != SAG_BF16) || d > 256 * vec_elems(dt)) return 0;
-    return norm_ws(norm_plan(n_rows, d, n_seg, false, dt), d, n_seg, groups, true, nullptr, 0).used;
+    return norm_ws(norm_plan(n_rows, d, n_seg, false, true, dt), d, n_seg, groups, true, nullptr, 0).used;
 }
 
 extern "C" sag_status sag_group_norm_backward(const void* X, int64_t ldx, int64_t n_rows, int64_t d, int64_t groups,
@@ -831,7 +979,7 @@ extern "C" sag_status sag_group_norm_backward(const void* X, int64_t ldx, int64_
     SAG_TRY(check_dense("group_norm G", G, n_rows, d, ldg, dt));
     if (dX) SAG_TRY(check_dense("group_norm dX", dX, n_rows, d, ldd, dt));
     if (n_seg > 0 && (!mean || !rstd)) return fail(SAG_E_INVALID, who + ": null mean or rstd");
-    const Plan p = norm_plan(n_rows, d, n_seg, !seg, dt);
+    const Plan p = norm_plan(n_rows, d, n_seg, !seg, true, dt);
     const Ws q = norm_ws(p, d, n_seg, groups, true, ws, ws_bytes);
     if (!ws || !aligned16(ws) || !q.fits) return fail(SAG_E_WORKSPACE, who + ": workspace too small");
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -844,8 +992,8 @@ extern "C" sag_status sag_group_norm_backward(const void* X, int64_t ldx, int64_
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.out = dX; a.ldo = ldd; a.g = G; a.ldg = ldg;
     a.piece = q.piece; a.stat = q.stat; a.col = dw || db ? q.col : nullptr;
-    a.rows_per_chunk = p.rows_per_chunk; a.n_chunks = p.n_chunks; a.short_rows = p.short_rows; a.graph_blocks = p.graph_blocks; a.tx = p.tx; a.ty = p.ty;
-    const unsigned first = static_cast<unsigned>(p.graph_blocks + p.chunk_blocks);
+    a.rows_per_chunk = p.rows_per_chunk; a.n_chunks = p.n_chunks; a.short_rows = p.short_rows; a.wave_rows = p.wave_rows; a.graph_blocks = p.graph_blocks; a.wave_blocks = p.wave_blocks; a.tx = p.tx; a.ty = p.ty;
+    const unsigned first = static_cast<unsigned>(p.blocks());
     const unsigned nc = static_cast<unsigned>(p.chunk_blocks);
     with_act(act, [&](auto ac) {
         constexpr int ACT = decltype(ac)::value;
@@ -854,7 +1002,8 @@ extern "C" sag_status sag_group_norm_backward(const void* X, int64_t ldx, int64_
             if (first)
                 by_column(a.gd % Vec<T>::N != 0, [&](auto cc) {
                     constexpr bool COL = decltype(cc)::value;
-                    const size_t lds = (static_cast<size_t>(2 * p.ty) * (d + slots_of<COL>(d, a.gd, p.tx, Vec<T>::N).n) + 2 * groups) * 4;
+                    const size_t lds = (static_cast<size_t>(2 * p.ty) * (d + slots_of<COL>(d, a.gd, p.tx, Vec<T>::N).n) + stat_floats(a)) * 4;
+                    set_group_lanes(a, slots_of<COL>(d, a.gd, p.tx, Vec<T>::N).per_group);
                     norm_bwd_first<T, ACT, COL><<<first, kThreads, lds, s>>>(a);
                 });
             if (dw || db)
