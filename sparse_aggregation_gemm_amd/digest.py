@@ -18,8 +18,16 @@ and pushes run on a second stream, ordered against the layers by events
 their pull, each push for the layer that produced its rows); without it
 every call runs on the current stream.  Both orders give the same bits.
 
-This module only orders calls into the library (halo gather, layer forward
-and backward, halo push); every step of the arithmetic runs in its kernels.
+With ``dropout`` each layer's input (local and halo rows) is dropped out before
+its aggregation, the stores keep the undropped rows, and the gradients pass
+the same mask before they go on or return to their owners.  The masks belong
+to the nodes' global ids, so a row has one mask in every partition that holds
+it, local or halo, and a step over partitions drops what a step over the
+whole graph does.
+
+This module only orders calls into the library (halo gather, dropout, layer
+forward and backward, halo push); every step of the arithmetic runs in its
+kernels.
 """
 from __future__ import annotations
 
@@ -54,15 +62,20 @@ class StaleExchange:
                  added to by the halo rows of each layer's input gradient.
     local_ids  : int32 global ids of the local rows (lo .. hi - 1), where the
                  pushes write.
+    dropout    : probability per layer of dropping a value of its input (None:
+                 no dropout; a layer of probability 0 runs as without).
+    seed       : of the masks.
     """
 
     def __init__(self, built: ops.Built, model: str, dims, relu, stores, grad_stores, local_ids,
-                 store_base: int = 0):
+                 store_base: int = 0, dropout=None, seed: int = 0):
         if model not in ("gcn", "sage"):
             raise ValueError("model must be gcn or sage")
         L = len(dims) - 1
         if len(stores) != L or len(grad_stores) != L or len(relu) != L:
             raise ValueError("one store, gradient store and ReLU flag per layer")
+        if dropout is not None and (len(dropout) != L or not all(0.0 <= p <= 1.0 for p in dropout)):
+            raise ValueError("one dropout probability in [0, 1] per layer")
         self.built, self.model, self.dims, self.relu = built, model, list(dims), list(relu)
         self.stores, self.grad_stores = stores, grad_stores
         self.local_ids = local_ids.to(torch.int32).contiguous()
@@ -75,6 +88,12 @@ class StaleExchange:
         # local rows of layer l + 1's input
         self.H = [ops.empty_dense(self.n_l + self.n_h, dims[l], dt, dev, fill=0.0) for l in range(L)]
         self.out = ops.empty_dense(self.n_l, dims[L], dt, dev)
+        # what layer l reads where it is dropped out: ReLU's backward needs
+        # the layer's own output, so the undropped rows stay
+        self.p = [0.0] * L if dropout is None else [float(p) for p in dropout]
+        self.seed = seed
+        self.dropped = [ops.empty_dense(self.n_l + self.n_h, dims[l], dt, dev) if self.p[l] > 0 else None for l in range(L)]
+        self.nodes = torch.cat([self.local_ids, built.halo_gid.to(torch.int32)]) if any(self.p) else None
         self.fwd = ops.gcn_layer_forward if model == "gcn" else ops.sage_layer_forward
         self.bwd = ops.gcn_layer_backward if model == "gcn" else ops.sage_layer_backward
         self.side = torch.cuda.Stream(device=dev)
@@ -82,15 +101,18 @@ class StaleExchange:
         self.e_end.record()
 
     def step(self, H0_local: torch.Tensor, W, b, G_out: torch.Tensor, overlap: bool = True,
-             want_dH0: bool = False) -> StepResult:
+             want_dH0: bool = False, call: int = 0) -> StepResult:
         """One forward + backward pass.  H0_local: the local input rows
         [n_local, d_0]; W, b: per-layer weights and fp32 biases; G_out: the
-        upstream gradient of the last layer's output."""
+        upstream gradient of the last layer's output; call: the step's number,
+        for masks of its own (layer l takes the generator's call call L + l,
+        modulo 2^32)."""
         L = len(self.dims) - 1
         n_l = self.n_l
         halo = self.built.halo_gid
         main = torch.cuda.current_stream()
         side = self.side if overlap else main
+        drops = [ops.Drop(p, self.seed, (call * L + l) % 2 ** 32, self.nodes) if p > 0 else None for l, p in enumerate(self.p)]
         pulled = [torch.cuda.Event() for _ in range(L)]
         produced = [torch.cuda.Event() for _ in range(L)]
         pushed = [torch.cuda.Event() for _ in range(L)]
@@ -106,7 +128,8 @@ class StaleExchange:
         for l in range(L):
             main.wait_event(pulled[l])
             Out = self.H[l + 1][:n_l] if l + 1 < L else self.out
-            _, _, ctx = self.fwd(self.built.A, self.H[l], W[l], b[l], relu=self.relu[l], Out=Out)
+            X = self.H[l] if drops[l] is None else ops.dropout(self.H[l], drops[l], Out=self.dropped[l])
+            _, _, ctx = self.fwd(self.built.A, X, W[l], b[l], relu=self.relu[l], Out=Out)
             ctxs.append(ctx)
             produced[l].record(main)
             if l + 1 < L:
@@ -122,6 +145,8 @@ class StaleExchange:
             want = l > 0 or want_dH0
             dW[l], db[l], dH = self.bwd(ctxs[l], self.built.AT, n_l, Y, g, want_dH=want)
             if want:
+                if drops[l] is not None:
+                    ops.dropout(dH, drops[l], Out=dH)
                 if self.n_h and self.grad_stores[l] is not None:
                     ops.halo_push(dH[n_l:], halo, self.grad_stores[l], row_base=self.base, accumulate=True)
                 g = dH[:n_l]
