@@ -578,12 +578,18 @@ __global__ __launch_bounds__(kThreads) void dense_dz(int64_t M, int64_t N, int64
 // matrix cores reduce over rows, so both operands come out of the row-major
 // tiles by the LDS transpose read ds_read_b64_tr_b16 (for four rows and
 // sixteen columns lane i of sixteen gets column i of the four rows).
-// A bf16 dZ alone would put 2^-9 into every term of an fp32 result, so dZ is
-// held as hi + lo (LO), both bf16, and multiplied twice; without an activation
-// or with ReLU, dZ is G or 0 exactly, up to the dropout scale, which the
-// reduction applies.  FROM_G: dZ comes from G and Z (z); otherwise hi and lo
+// A bf16 dZ alone would put 2^-8 into every term of an fp32 result, so dZ is
+// held as two bf16 parts (PARTS) and multiplied twice: 2^-16 a term, 2.4e-6
+// of the result in the 2-norm, which is what fp32 sums of 50,000 terms are off
+// by.  Below kFineRows rows a third part takes that to 1e-7.  Its tiles leave
+// LDS room for one stage instead of two (the whole backward pass with GELU, two
+// parts -> three: 2700 x 256 -> 256 29.1 us both, 32767 x 256 -> 256 49 -> 53,
+// 10000 x 602 -> 128 38 -> 40, 10000 x 1500 -> 512, which computes dZ once a
+// block of 256 inputs, 118 -> 158).  Without an activation or with ReLU, dZ is
+// G or 0 exactly, up to the dropout scale, which the reduction applies.  FROM_G: dZ comes from G and Z (z); otherwise hi and lo
 // are read.  Column sums (db) are taken of the fp32 dZ on its way into LDS.
 constexpr int kTnWaves = 16, kTnThreads = kTnWaves * 64, kTnK = 256, kTnN = 128, kTnRows = 64;
+constexpr int64_t kFineRows = 32768;
 constexpr int kTnPX = kTnK * 2 + 64, kTnPZ = kTnN * 2 + 64;     // row pitches in LDS: 16 banks a row apart
 
 struct TnArgs {
@@ -603,13 +609,13 @@ struct TnArgs {
 template <int ACT>
 constexpr bool dz_exact() { return ACT == SAG_ACT_NONE || ACT == SAG_ACT_RELU; }
 
-template <int ACT, bool DROP, bool LO, bool FROM_G>
+template <int ACT, bool DROP, int PARTS, bool FROM_G>
 __global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
     typedef short i16x4_t __attribute__((ext_vector_type(4)));
     constexpr int SX = kTnRows * kTnPX, SZ = kTnRows * kTnPZ;
-    constexpr int STAGE = SX + (LO ? 2 : 1) * SZ;
+    constexpr int STAGE = SX + PARTS * SZ, STAGES = PARTS == 3 ? 1 : 2;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-    float* tab = reinterpret_cast<float*>(lds + 2 * STAGE);
+    float* tab = reinterpret_cast<float*>(lds + STAGES * STAGE);
     if constexpr (FROM_G) build_table<ACT>(tab, DROP ? p.drop.scale : 1.f, threadIdx.x, kTnThreads);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wk = wave >> 2, wn = wave & 3;
@@ -635,7 +641,7 @@ __global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
     const char* pg = reinterpret_cast<const char*>(p.g + (m_begin + zr) * p.ldg + zcol);
     const char* pz = reinterpret_cast<const char*>(p.z + (m_begin + zr) * p.ldz + zcol);
     const int64_t half_x = 64 * p.ldx, step_g = 128 * p.ldg, step_z = 128 * p.ldz;   // bytes: 32 rows, 64 rows
-    constexpr bool kReadZ = FROM_G ? ACT != SAG_ACT_NONE : LO;
+    constexpr bool kReadZ = FROM_G ? ACT != SAG_ACT_NONE : PARTS == 2;
     auto load = [&](int64_t m) __attribute__((always_inline)) {
         rx[0] = load16(m + xr < m_end ? px : reinterpret_cast<const char*>(p.x));
         rx[1] = load16(m + xr + 32 < m_end ? px + half_x : reinterpret_cast<const char*>(p.x));
@@ -670,23 +676,25 @@ __global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
                 f[e] = in ? f[e] : 0.f;
                 cs[e] += f[e];
             }
-            const u32x4_t hi = pack8(f);
-            store16(Hs + zr * kTnPZ + zc * 2, hi);
-            if constexpr (LO) {
-                float hf[8];
-                unpack<uint16_t>(as_uint4(hi), hf);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] -= hf[e];
-                store16(Hs + SZ + zr * kTnPZ + zc * 2, pack8(f));
+            for (int q = 0; q < PARTS; ++q) {
+                const u32x4_t part = pack8(f);
+                store16(Hs + q * SZ + zr * kTnPZ + zc * 2, part);
+                if (q + 1 < PARTS) {
+                    float hf[8];
+                    unpack<uint16_t>(as_uint4(part), hf);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] -= hf[e];
+                }
             }
         } else {
-            const u32x4_t hi = in ? rg : none, lo = LO && in ? rz : none;
+            const u32x4_t hi = in ? rg : none, lo = PARTS == 2 && in ? rz : none;
             float f[8];
             unpack<uint16_t>(as_uint4(hi), f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) cs[e] += f[e];
             store16(Hs + zr * kTnPZ + zc * 2, hi);
-            if constexpr (LO) {
+            if constexpr (PARTS == 2) {
                 unpack<uint16_t>(as_uint4(lo), f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) cs[e] += f[e];
@@ -715,28 +723,37 @@ __global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) xa[i] = frag(Xs + m * kTnPX + (wk * 64 + 32 * i + c) * 2, kTnPX);
             const unsigned char* h = Hs + m * kTnPZ + (wn * 32 + c) * 2;
-            if constexpr (LO) {
-                const bf16x8_t yl = frag(h + SZ, kTnPZ);
+            // (the smallest part first)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], yl, acc[i], 0, 0, 0);
+            for (int q = PARTS - 1; q >= 0; --q) {
+                const bf16x8_t y = frag(h + q * SZ, kTnPZ);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], y, acc[i], 0, 0, 0);
             }
-            const bf16x8_t yb = frag(h, kTnPZ);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], yb, acc[i], 0, 0, 0);
         }
     };
     const int64_t steps = (m_end - m_begin + kTnRows - 1) / kTnRows;
     load(m_begin);
-    store(0, m_begin);
-    load(m_begin + kTnRows);
-    __syncthreads();
-    // step s: stage s + 1, load s + 2, multiply s (past the chunk zeros are staged)
-    for (int64_t s = 0; s < steps; ++s) {
-        const int cur = static_cast<int>(s & 1);
-        store(cur ^ 1, m_begin + (s + 1) * kTnRows);
-        load(m_begin + (s + 2) * kTnRows);
-        multiply(cur);
+    if constexpr (STAGES == 1) {
+        for (int64_t s = 0; s < steps; ++s) {
+            store(0, m_begin + s * kTnRows);
+            load(m_begin + (s + 1) * kTnRows);
+            __syncthreads();
+            multiply(0);
+            __syncthreads();
+        }
+    } else {
+        store(0, m_begin);
+        load(m_begin + kTnRows);
         __syncthreads();
+        // step s: stage s + 1, load s + 2, multiply s (past the chunk zeros are staged)
+        for (int64_t s = 0; s < steps; ++s) {
+            const int cur = static_cast<int>(s & 1);
+            store(cur ^ 1, m_begin + (s + 1) * kTnRows);
+            load(m_begin + (s + 2) * kTnRows);
+            multiply(cur);
+            __syncthreads();
+        }
     }
     const int64_t pn = p.n_nblk * kTnN;
     float* out = p.part + (chunk * p.n_kblk * kTnK + k0 + wk * 64 + 4 * (lane / 32)) * pn + n0 + wn * 32 + lane % 32;
@@ -922,7 +939,7 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, sag_dtype dt, void* ws, size_t byt
     w.bp = c.take<char>(pack_bytes(N, K, dt));
     if (!dz_from_g(K, dt)) w.hi = c.take<char>(dense_bytes(M, N, dt));
     if (dt == SAG_BF16) {
-        if (!dz_from_g(K, dt)) w.lo = c.take<char>(dense_bytes(M, N, dt));
+        if (!dz_from_g(K, dt) && M >= kFineRows) w.lo = c.take<char>(dense_bytes(M, N, dt));
         const TnPlan p = tn_plan(M, K, N);
         w.part = c.take<float>(p.chunks * p.n_kblk * kTnK * p.n_nblk * kTnN);
         w.part_cs = c.take<float>(p.chunks * p.n_nblk * kTnN);
@@ -936,16 +953,16 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, sag_dtype dt, void* ws, size_t byt
     return w;
 }
 
-template <int ACT, bool DROP, bool LO, bool FROM_G>
+template <int ACT, bool DROP, int PARTS, bool FROM_G>
 sag_status launch_tn(const TnArgs& a, int64_t chunks, hipStream_t s) {
-    constexpr int lds = 2 * (kTnRows * kTnPX + (LO ? 2 : 1) * kTnRows * kTnPZ) +
+    constexpr int lds = (PARTS == 3 ? 1 : 2) * (kTnRows * kTnPX + PARTS * kTnRows * kTnPZ) +
                         (FROM_G && uses_table<ACT>() ? kTabSize * 4 : 0);
     static_assert(lds >= kTnRows * kTnN * 4, "column-sum buffer");
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_tn<ACT, DROP, LO, FROM_G>),
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_tn<ACT, DROP, PARTS, FROM_G>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     SAG_CHECK_HIP(attr);
     const unsigned grid = static_cast<unsigned>(chunks * a.n_kblk * a.n_nblk);
-    dense_tn<ACT, DROP, LO, FROM_G><<<grid, kTnThreads, lds, s>>>(a);
+    dense_tn<ACT, DROP, PARTS, FROM_G><<<grid, kTnThreads, lds, s>>>(a);
     SAG_LAUNCH_CHECK();
     return SAG_OK;
 }
@@ -961,17 +978,23 @@ sag_status tn_run(sag_act act, TnArgs a, bool from_g, float* dW, float* db, cons
     if (exact) a.drop.scale = 1.f;
     TraceScope trace(trace_enabled() ? shape_name("dense_dw", "bf16", a.M, a.K, a.N) : std::string(), s,
                      2 * (a.M * a.K + a.M * a.N * (act == SAG_ACT_NONE || (exact && !from_g) ? 1 : 2)) + 4 * (a.K * a.N + a.N),
-                     (exact ? 2 : 4) * a.M * a.K * a.N);
+                     (exact ? 2 : (from_g && a.M < kFineRows ? 6 : 4)) * a.M * a.K * a.N);
     if (p.chunks) {
         sag_status st = SAG_OK;
         if (!from_g) {
-            st = exact ? launch_tn<SAG_ACT_NONE, false, false, false>(a, p.chunks, s)
-                       : launch_tn<SAG_ACT_NONE, false, true, false>(a, p.chunks, s);
+            st = exact ? launch_tn<SAG_ACT_NONE, false, 1, false>(a, p.chunks, s)
+                       : launch_tn<SAG_ACT_NONE, false, 2, false>(a, p.chunks, s);
         } else {
             with_act(act, [&](auto ac) {
                 constexpr int ACT = decltype(ac)::value;
-                st = a.drop.T ? launch_tn<ACT, true, !dz_exact<ACT>(), true>(a, p.chunks, s)
-                              : launch_tn<ACT, false, !dz_exact<ACT>(), true>(a, p.chunks, s);
+                auto go = [&](auto parts) {
+                    constexpr int PARTS = decltype(parts)::value;
+                    return a.drop.T ? launch_tn<ACT, true, PARTS, true>(a, p.chunks, s)
+                                    : launch_tn<ACT, false, PARTS, true>(a, p.chunks, s);
+                };
+                if constexpr (dz_exact<ACT>()) st = go(std::integral_constant<int, 1>{});
+                else if (a.M < kFineRows) st = go(std::integral_constant<int, 3>{});
+                else st = go(std::integral_constant<int, 2>{});
             });
         }
         SAG_TRY(st);
@@ -991,8 +1014,10 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
     const bool from_g = dz_from_g(K, dt), exact = act == SAG_ACT_NONE || act == SAG_ACT_RELU;
     T* hi = static_cast<T*>(w.hi);
     T* lo = exact ? nullptr : static_cast<T*>(w.lo);
+    // the weight gradient of few rows takes three parts of dZ, which are made of G and Z
+    const bool dw_from_g = from_g || (dt == SAG_BF16 && !exact && M < kFineRows);
     // (the tiled input gradient reads a stored dZ, and so does the weight gradient)
-    if (M > 0 && !from_g && ((dX && !few_tiles(M, K)) || dW || db)) {
+    if (M > 0 && !from_g && ((dX && !few_tiles(M, K)) || (!dw_from_g && (dW || db)))) {
         const int64_t blocks = cdiv(M * upr, kThreads);
         if (blocks >= (1 << 24)) return fail(SAG_E_UNSUPPORTED, "dense backward: too many elements for one launch");
         TraceScope trace(trace_enabled() ? shape_name("dense_dz", dt == SAG_BF16 ? "bf16" : "f32", M, N, 0) : std::string(),
@@ -1030,9 +1055,9 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
     if constexpr (sizeof(T) == 2) {
         TnArgs a{};
         a.x = X; a.ldx = ldx; a.M = M; a.K = K; a.N = N; a.slope = slope; a.drop = drop;
-        a.g = from_g ? G : hi; a.ldg = from_g ? ldg : ldh;
-        a.z = from_g ? Z : lo; a.ldz = from_g ? ldz : ldh;
-        return tn_run(act, a, from_g, dW, db, w, s);
+        a.g = dw_from_g ? G : hi; a.ldg = dw_from_g ? ldg : ldh;
+        a.z = dw_from_g ? Z : lo; a.ldz = dw_from_g ? ldz : ldh;
+        return tn_run(act, a, dw_from_g, dW, db, w, s);
     } else {
         GemmA a;
         a.a1 = X; a.lda1 = ldx; a.k1 = K; a.m1 = M;

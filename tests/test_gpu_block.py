@@ -181,7 +181,8 @@ def test_dense_backward(dt, M, K, N, kind, p):
     x, w, z, gg = f64(X), f64(W), f64(Z), f64(G)
     dZ, rW, rb, rX = ob.dense_backward(x, w, z, kind, 0.1, f, gg)
     ez = np.abs(gg) * f * (16 * U * (1 + np.abs(z)) if kind in ("gelu", "silu") else 0) + 3 * U * np.abs(dZ)
-    keep = 2.0 ** -16 if dt == "bf16" else 0.0     # two bf16 parts: (2^-8)^2
+    # dZ in the weight gradient's products: three bf16 parts, (2^-8)^3, or two from 2^15 rows on; exact without rounding
+    keep = 0.0 if dt == "f32" or kind in ("none", "relu") else (2.0 ** -24 if M < 2 ** 15 else 2.0 ** -16)
     within(dX, rX, ((ez + (UT[dt] if dt == "bf16" else 0) * np.abs(dZ)) @ np.abs(w).T + N * U * np.abs(dZ) @ np.abs(w).T) * 1.01
            + UT[dt] * np.abs(rX) * 1.01 + 1e-30)
     within(dW, rW, np.abs(x).T @ (ez + keep * np.abs(dZ)) + (M + 2) * U * np.abs(x).T @ np.abs(dZ) + 1e-30)

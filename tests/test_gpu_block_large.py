@@ -16,7 +16,8 @@ from gpu_util import DEV, f64, say, to_dev  # noqa: E402
 # Out of 64 columns or fewer, of more, of several tiles across; ragged in each size
 FORWARD = [(9001, 33, 64), (8200, 1, 40), (2100, 70, 300), (1025, 130, 1000), (70, 65, 8200), (4200, 256, 128)]
 # dX of up to 64, 128, 256 and more columns (bf16 beyond 256 stores dZ)
-BACKWARD = [(9001, 40, 16), (17000, 7, 3), (5000, 100, 72), (3001, 200, 65), (2500, 256, 300), (1500, 400, 130), (515, 1030, 33)]
+BACKWARD = [(9001, 40, 16), (17000, 7, 3), (5000, 100, 72), (3001, 200, 65), (2500, 256, 300), (1500, 400, 130), (515, 1030, 33),
+            (33000, 40, 33), (33000, 300, 20)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
