@@ -361,14 +361,14 @@ __global__ __launch_bounds__((BN == 256 ? 512 : 256), GRAD ? (BN == 256 ? 4 : 3)
 
 // ---- few tiles ---------------------------------------------------------------------------
 // The same product where 32 x 32 tiles do not fill the chip: a workgroup of
-// up to sixteen wavefronts does one tile, each wavefront every sixteenth
-// 128-byte piece of k, and their sums are added in LDS in a fixed tree before
+// up to sixteen wavefronts does one tile (of 32 x 32, or 16 x 16), each
+// wavefront every sixteenth piece of k, 128 bytes (256), and their sums are added in LDS in a fixed tree before
 // the epilogue.  Operands go from memory straight into the matrix cores'
 // registers, B from the weight as it lies (two bytes or four a load for the
 // forward product, whole vectors along the rows for the gradient's), so there
 // is one launch, no workspace and one round of loads in front of the products.
 // What bounds it is latency: launch, one memory round trip and the tree.
-constexpr int kFewPitch = 36;              // floats of a tile row in LDS
+constexpr int kSmallTiles = 128;           // up to half as many as CUs: see small_tiles
 constexpr int kFewTiles = 512;             // taken up to two workgroups a CU
 
 // Sixteen bytes from an address aligned to an element.
@@ -378,24 +378,26 @@ __device__ __forceinline__ u32x4_t load16_any(const T* p) {
     return reinterpret_cast<const Any*>(p)->v;
 }
 
-template <class T, int ACT, bool DROP, bool GRAD>
+template <int TE> constexpr int few_pitch() { return TE + 4; }             // floats of a tile row in LDS
+template <class T, int TE> constexpr int few_piece() { return 4 * (64 / TE) * Vec<T>::N; }   // k a wavefront takes at once
+
+template <class T, int ACT, bool DROP, bool GRAD, int TE>
 __global__ __launch_bounds__(1024) void dense_few(NnArgs<T> p, const T* __restrict__ w, int64_t ldw) {
-    constexpr int V = Vec<T>::N;
-    constexpr int CK = kRowB / static_cast<int>(sizeof(T));
-    extern __shared__ __attribute__((aligned(16))) float part[];   // [wavefront][32][kFewPitch]
+    constexpr int V = Vec<T>::N, CK = few_piece<T, TE>(), PITCH = few_pitch<TE>();
+    extern __shared__ __attribute__((aligned(16))) float part[];   // [wavefront][TE][PITCH]
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = blockDim.x >> 6;
-    const int h = lane >> 5, l32 = lane & 31;
+    const int h = lane / TE, lt = lane % TE;
     const uint32_t tm = blockIdx.x / static_cast<uint32_t>(p.n_blk), tn = blockIdx.x % static_cast<uint32_t>(p.n_blk);
-    const int64_t m0 = static_cast<int64_t>(tm) * 32, n0 = static_cast<int64_t>(tn) * 32;
-    const int64_t row = m0 + l32 < p.M ? m0 + l32 : p.M - 1, col = n0 + l32 < p.N ? n0 + l32 : p.N - 1;
+    const int64_t m0 = static_cast<int64_t>(tm) * TE, n0 = static_cast<int64_t>(tn) * TE;
+    const int64_t row = m0 + lt < p.M ? m0 + lt : p.M - 1, col = n0 + lt < p.N ? n0 + lt : p.N - 1;
     uint32_t call = 0, node = 0;
     if constexpr (DROP) call = p.drop.call_now();
     if constexpr (DROP && GRAD) node = p.drop.node_of(row);
     const T* ar = p.a + row * p.lda;
     const T* zr = GRAD && ACT != SAG_ACT_NONE ? p.az + row * p.ldaz : nullptr;
-    f32x16_t acc;
+    std::conditional_t<TE == 32, f32x16_t, f32x4_t> acc;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+    for (int r = 0; r < TE * TE / 64; ++r) acc[r] = 0.f;
     for (int64_t k0 = static_cast<int64_t>(wave) * CK; k0 < p.K; k0 += static_cast<int64_t>(waves) * CK) {
         u32x4_t a[4], z[4], b[4];
 #pragma unroll
@@ -454,7 +456,7 @@ __global__ __launch_bounds__(1024) void dense_few(NnArgs<T> p, const T* __restri
                     for (int e = 0; e < V; ++e) {
                         // (four fp32 columns are one half of a block's eight)
                         if constexpr (V == 8) f[e] = p.drop.apply(f[e], dw, e);
-                        else f[e] = h ? p.drop.apply(f[e], dw, e + 4) : p.drop.apply(f[e], dw, e);
+                        else f[e] = h & 1 ? p.drop.apply(f[e], dw, e + 4) : p.drop.apply(f[e], dw, e);
                     }
                 }
                 if constexpr (V == 8) a[s] = u32x4_t{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
@@ -462,29 +464,33 @@ __global__ __launch_bounds__(1024) void dense_few(NnArgs<T> p, const T* __restri
             }
             if (left < V) a[s] = keep_first<T>(a[s], left);
             if constexpr (sizeof(T) == 2) {
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, b[s]),
-                                                              __builtin_bit_cast(bf16x8_t, a[s]), acc, 0, 0, 0);
+                const bf16x8_t bb = __builtin_bit_cast(bf16x8_t, b[s]), aa = __builtin_bit_cast(bf16x8_t, a[s]);
+                if constexpr (TE == 32) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bb, aa, acc, 0, 0, 0);
+                else acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bb, aa, acc, 0, 0, 0);
             } else {
                 const f32x4_t bb = __builtin_bit_cast(f32x4_t, b[s]), aa = __builtin_bit_cast(f32x4_t, a[s]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bb[q], aa[q], acc, 0, 0, 0);
+                for (int q = 0; q < 4; ++q) {
+                    if constexpr (TE == 32) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bb[q], aa[q], acc, 0, 0, 0);
+                    else acc = __builtin_amdgcn_mfma_f32_16x16x4f32(bb[q], aa[q], acc, 0, 0, 0);
+                }
             }
         }
     }
-    float* mine = part + wave * 32 * kFewPitch;
+    float* mine = part + wave * TE * PITCH;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4*>(mine + l32 * kFewPitch + 8 * q + 4 * h) =
+    for (int q = 0; q < TE * TE / 256; ++q)
+        *reinterpret_cast<float4*>(mine + lt * PITCH + 8 * q + 4 * h) =
             make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
     __syncthreads();
     // units of eight columns, four lanes to a unit, each every fourth wavefront's sum
-    for (int unit = t >> 2; unit < 128; unit += blockDim.x >> 2) {
-        const int r = unit >> 2, u = unit & 3;
+    for (int unit = t >> 2; unit < TE * TE / 8; unit += blockDim.x >> 2) {
+        const int r = unit / (TE / 8), u = unit % (TE / 8);
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = 0.f;
         for (int v = t & 3; v < waves; v += 4) {
-            const float* src = part + (v * 32 + r) * kFewPitch + u * 8;
+            const float* src = part + (v * TE + r) * PITCH + u * 8;
             const float4 lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
             y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
             y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
@@ -827,30 +833,40 @@ size_t pack_bytes(int64_t K, int64_t N, sag_dtype dt) {
 
 bool few_tiles(int64_t M, int64_t N) { return cdiv(M, 32) * cdiv(N, 32) <= kFewTiles; }
 
-// The product by 32 x 32 tiles; W as it lies (rows of ldw).
+// Tiles of 16 x 16 where those of 32 leave half the CUs idle or half of every
+// tile empty.  They read the operands twice as often, and four times as many
+// compute units read them: 2708 x 1433 -> 16 fp32 (85 tiles of 32) 15.5 -> 7.8
+// us, 1000 x 512 -> 128 bf16 (128) 5.6 -> 5.2, 16000 x 256 -> 16 bf16 (500) 6.4
+// -> 5.1, but 512 x 2000 -> 512 bf16 (256) 11.8 -> 21 and 4000 x 256 -> 128 fp32
+// (500) 8.3 -> 11.
+bool small_tiles(int64_t M, int64_t N) { return M <= 16 || N <= 16 || cdiv(M, 32) * cdiv(N, 32) <= kSmallTiles; }
+
+// The product of few tiles; W as it lies (rows of ldw).
 template <class T, bool GRAD>
 sag_status few_run(const char* what, sag_act act, NnArgs<T> p, const T* w, int64_t ldw, sag_dtype dt, hipStream_t s) {
-    p.n_blk = cdiv(p.N, 32);
-    p.m_blk = cdiv(p.M, 32);
-    const int64_t pieces = cdiv(p.K, kRowB / static_cast<int64_t>(sizeof(T)));
-    const int waves = static_cast<int>(pieces < 16 ? pieces : 16);
     TraceScope trace(trace_enabled() ? shape_name(what, dt == SAG_BF16 ? "bf16" : "f32", p.M, p.K, p.N) : std::string(),
                      s, elt_size(dt) * (p.M * p.K * (p.az ? 2 : 1) + p.M * p.N * (1 + (p.z ? 1 : 0) + (p.res ? 1 : 0)) + p.K * p.N),
                      2 * p.M * p.K * p.N);
-    const unsigned grid = static_cast<unsigned>(p.n_blk * p.m_blk);
-    const size_t lds = static_cast<size_t>(waves) * 32 * kFewPitch * 4;
     sag_status st = SAG_OK;
     with_act(act, [&](auto ac) {
         constexpr int ACT = decltype(ac)::value;
-        auto go = [&](auto drop_c) -> sag_status {
+        auto go = [&](auto drop_c, auto edge_c) -> sag_status {
             constexpr bool DROP = decltype(drop_c)::value;
-            static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_few<T, ACT, DROP, GRAD>),
-                                                               hipFuncAttributeMaxDynamicSharedMemorySize, 16 * 32 * kFewPitch * 4);
+            constexpr int TE = decltype(edge_c)::value, kWaveLds = TE * few_pitch<TE>() * 4;
+            static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_few<T, ACT, DROP, GRAD, TE>),
+                                                               hipFuncAttributeMaxDynamicSharedMemorySize, 16 * kWaveLds);
             SAG_CHECK_HIP(attr);
-            dense_few<T, ACT, DROP, GRAD><<<grid, waves * 64, lds, s>>>(p, w, ldw);
+            p.n_blk = cdiv(p.N, TE);
+            p.m_blk = cdiv(p.M, TE);
+            const int64_t pieces = cdiv(p.K, few_piece<T, TE>());
+            const int waves = static_cast<int>(pieces < 16 ? pieces : 16);
+            dense_few<T, ACT, DROP, GRAD, TE><<<static_cast<unsigned>(p.n_blk * p.m_blk), waves * 64, waves * kWaveLds, s>>>(p, w, ldw);
             return SAG_OK;
         };
-        st = p.drop.T ? go(std::true_type{}) : go(std::false_type{});
+        auto edge = [&](auto drop_c) {
+            return small_tiles(p.M, p.N) ? go(drop_c, std::integral_constant<int, 16>{}) : go(drop_c, std::integral_constant<int, 32>{});
+        };
+        st = p.drop.T ? edge(std::true_type{}) : edge(std::false_type{});
     });
     SAG_TRY(st);
     SAG_LAUNCH_CHECK();
