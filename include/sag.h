@@ -651,7 +651,7 @@ sag_status sag_dropout(const void* X, int64_t ldx, int64_t n, int64_t d, sag_dty
  * backward call needs it unless act is SAG_ACT_NONE); Out: [M, N].  X, W, R,
  * Z and Out of type dt, sums in fp32, each output rounded once (act sees the
  * unrounded Z).  K, N >= 1; M may be 0.  Out may be R (same pointer and ld).
- * K and N have no limit below 2^24.  A product of few tiles needs no
+ * The other outputs overlap no input.  K and N have no limit below 2^24.  A product of few tiles needs no
  * workspace (the query returns 0; ws may be NULL). */
 size_t sag_dense_forward_workspace_bytes(int64_t M, int64_t K, int64_t N, sag_dtype dt);
 sag_status sag_dense_layer_forward(int64_t M, const void* X, int64_t ldx, int64_t K, const void* W, const float* b,
@@ -663,8 +663,11 @@ sag_status sag_dense_layer_forward(int64_t M, const void* X, int64_t ldx, int64_
  *   dZ = act'(Z) dropout(G);  dX = dZ W^T ([M, K], type dt, nullable);
  *   dW = X^T dZ (fp32 [K, N], ld N, nullable);  db = column sums of dZ
  *   (fp32[N], nullable).
- * act, slope and drop have to be the forward's.  dW and db are held to fp32
- * throughout for bf16 operands too; dX takes dZ rounded to dt. */
+ * act, slope and drop have to be the forward's.  dX takes dZ rounded to dt.
+ * dW and db of bf16 operands are fp32 results: where an activation makes dZ
+ * inexact in bf16 it enters their sums as three bf16 parts (2^-24 of a term),
+ * or from 32768 rows on, where fp32 sums are off by more, as two (2^-16).
+ * Outputs overlap no input.  A bf16 workspace for M rows serves fewer too. */
 size_t sag_dense_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, sag_dtype dt);
 sag_status sag_dense_layer_backward(int64_t M, const void* X, int64_t ldx, int64_t K, const void* W, int64_t N,
                                     sag_act act, float slope, const sag_drop* drop, const void* Z, int64_t ldz,

@@ -11,7 +11,10 @@
 // of eight consecutive columns: one generator block, one 16-byte vector of
 // R, Z and Out each, and whole 128-byte lines of a row per eight lanes.
 // B (the weight, or its transpose) is packed first into [N, K] with K
-// contiguous and zeros up to whole tiles, so only A needs bounds.
+// contiguous and zeros up to whole tiles, so only A needs bounds.  Products of
+// few tiles run in dense_few, the weight gradients in dense_tn (bf16) and
+// dense_tn32 (fp32).  2.45M x 256 -> 256 bf16 with GELU, dropout, residual and
+// Z: 1.19 ms forward (4.2 TB/s), 2.05 ms backward.
 #include <type_traits>
 
 #include "drop.h"
@@ -27,16 +30,6 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 // (a vector type, not the uint4 class, whose conditional copies go through
 // private memory)
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
-// Calls f(std::integral_constant<int, I>) for I in [B, E): register arrays
-// indexed by I stay in registers.
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-    if constexpr (B < E) {
-        f(std::integral_constant<int, B>{});
-        static_for<B + 1, E>(f);
-    }
-}
 
 constexpr int kThreads = 256;
 constexpr int kRowB = 128;                 // bytes of k per tile row
@@ -784,6 +777,133 @@ __global__ __launch_bounds__(kTnThreads, 4) void dense_tn(TnArgs p) {
     }
 }
 
+// ---- dW (fp32) ---------------------------------------------------------------------------
+// The same product of fp32 X and stored fp32 dZ: 128 rows of C (columns of X)
+// by 32 NB WN columns, four wavefronts of WN x NB tiles of 32 x 32 each, 32
+// rows a step through LDS (two stages, one barrier a step, the next step's
+// loads in registers), two workgroups a CU.  The fp32 matrix instruction
+// takes one value a lane and operand, adjacent lanes adjacent columns, so the
+// row-major tiles are read as they lie; rows are 32 banks apart, as a lane's
+// upper half reads the next row.  What bounds it is the matrix cores.
+// Blocks of 128 inputs, not 256: 602 take five of them (640) where three of 256
+// would be 768.  232965 x 602 -> 128: 409 us (93 TFLOP/s of products, 70% of the
+// matrix cores' cycles; bytes alone would take 130).  With tiles of 32 and 64
+// columns for narrow layers the whole backward pass takes, against the plain
+// product's weight-gradient kernel (256 inputs a block, four times the chunks):
+// 232965 x 602 -> 128 908 -> 842 us, 232965 x 562 -> 17 484 -> 387,
+// 2800 x 562 -> 17 42 -> 25, 25000 x 100 -> 47 58 -> 39, 232965 x 256 -> 256 702
+// -> 724.
+constexpr int kT32K = 128, kT32Rows = 32, kT32PX = kT32K + 32;
+
+struct Tn32Args {
+    const float *x, *z;         // z: dZ
+    int64_t ldx, ldz, M, K, N, n_kblk, n_nblk, rows_per_chunk;
+    float* part;                // [chunk][n_kblk * 128][n_nblk * TN]
+    float* part_cs;             // [chunk][n_nblk * TN], nullable
+};
+
+template <int NB, int WN>
+__global__ __launch_bounds__(256, 2) void dense_tn32(Tn32Args p) {
+    constexpr int TN = 32 * NB * WN, KB = WN, PZ = TN + 32;
+    constexpr int SX = kT32Rows * kT32PX, STAGE = SX + kT32Rows * PZ;
+    constexpr int UZ = TN / 32, ZT = TN / 4;        // vectors of dZ a thread, threads across its row
+    __shared__ __attribute__((aligned(16))) float lds[2 * STAGE];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5, l32 = lane & 31;
+    const int wk = wave / WN, wn = wave % WN;
+    const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int64_t nb = tile % p.n_nblk, kb = tile / p.n_nblk % p.n_kblk, chunk = tile / (p.n_nblk * p.n_kblk);
+    const int64_t k0 = kb * kT32K, n0 = nb * TN;
+    const int64_t m_begin = chunk * p.rows_per_chunk;
+    const int64_t m_end = m_begin + p.rows_per_chunk < p.M ? m_begin + p.rows_per_chunk : p.M;
+    const int xr = t >> 5, xc = (t & 31) * 4, zr = t / ZT, zc = t % ZT * 4;
+    const int64_t xlast = (p.K + 3) / 4 * 4 - 4, zlast = (p.N + 3) / 4 * 4 - 4;
+    const float* px = p.x + (k0 + xc < xlast ? k0 + xc : xlast);
+    const float* pz = p.z + (n0 + zc < zlast ? n0 + zc : zlast);
+    u32x4_t rx[4], rz[UZ];
+    // (a row past the chunk is the chunk's first, and staged as zeros)
+    auto load = [&](int64_t m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rx[i] = load16(px + (m + xr + 8 * i < m_end ? m + xr + 8 * i : m_begin) * p.ldx);
+#pragma unroll
+        for (int i = 0; i < UZ; ++i) {
+            const int64_t r = m + zr + 256 / ZT * i;
+            rz[i] = load16(pz + (r < m_end ? r : m_begin) * p.ldz);
+        }
+    };
+    float cs[4] = {0.f, 0.f, 0.f, 0.f};
+    auto store = [&](int st, int64_t m) __attribute__((always_inline)) {
+        float* Xs = lds + st * STAGE;
+        float* Zs = Xs + SX;
+        const u32x4_t none = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store16(Xs + (xr + 8 * i) * kT32PX + xc, m + xr + 8 * i < m_end ? rx[i] : none);
+#pragma unroll
+        for (int i = 0; i < UZ; ++i) {
+            const int r = zr + 256 / ZT * i;
+            const u32x4_t v = m + r < m_end ? rz[i] : none;
+            store16(Zs + r * PZ + zc, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) cs[e] += __uint_as_float(v[e]);
+        }
+    };
+    f32x16_t acc[KB][NB];
+#pragma unroll
+    for (int i = 0; i < KB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const int64_t steps = (m_end - m_begin + kT32Rows - 1) / kT32Rows;
+    load(m_begin);
+    store(0, m_begin);
+    load(m_begin + kT32Rows);
+    __syncthreads();
+    // step s: stage s + 1, load s + 2, multiply s (past the chunk zeros are staged)
+    for (int64_t s = 0; s < steps; ++s) {
+        const int cur = static_cast<int>(s & 1);
+        store(cur ^ 1, m_begin + (s + 1) * kT32Rows);
+        load(m_begin + (s + 2) * kT32Rows);
+        const float* Xs = lds + cur * STAGE + h * kT32PX + wk * 32 * KB + l32;
+        const float* Zs = lds + cur * STAGE + SX + h * PZ + wn * 32 * NB + l32;
+#pragma unroll
+        for (int q = 0; q < kT32Rows / 2; ++q) {
+            float a[KB], b[NB];
+#pragma unroll
+            for (int i = 0; i < KB; ++i) a[i] = Xs[2 * q * kT32PX + 32 * i];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) b[j] = Zs[2 * q * PZ + 32 * j];
+#pragma unroll
+            for (int i = 0; i < KB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
+        __syncthreads();
+    }
+    const int64_t pn = p.n_nblk * TN;
+#pragma unroll
+    for (int i = 0; i < KB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            float* out = p.part + (chunk * p.n_kblk * kT32K + k0 + (wk * KB + i) * 32 + 4 * h) * pn + n0 + (wn * NB + j) * 32 + l32;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                *out = acc[i][j][r];
+                out += r % 4 == 3 ? 5 * pn : pn;
+            }
+        }
+    if (p.part_cs && kb == 0) {
+        // the row threads of each column, in order
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lds[zr * TN + zc + e] = cs[e];
+        __syncthreads();
+        if (t < TN) {
+            float sum = 0.f;
+            for (int r = 0; r < 256 / ZT; ++r) sum += lds[r * TN + t];
+            p.part_cs[chunk * pn + n0 + t] = sum;
+        }
+    }
+}
+
 // dW and db: the partials in chunk order, four threads to an element, each a
 // quarter of the chunks, eight loads ahead; times the dropout scale where the
 // sums are of G itself.
@@ -919,33 +1039,41 @@ sag_status forward_typed(NnArgs<T> p, const void* W, sag_act act, sag_dtype dt, 
 // bf16 layers of up to 256 inputs never store dZ: the input gradient and the
 // weight gradient each compute it from G and Z on its way into LDS (once a
 // row, as 256 columns make one block in both).  Wider ones would compute it
-// once a block of 256, where it costs more than the products (45 operations
+// once a block of 256, where it costs more than the products (some 35 operations
 // an element against 0.25 matrix operations' time a column block), so there it
 // is stored first, as hi (and lo, where it is not exact); fp32, bound by the
 // matrix cores, stores it as well.
 bool dz_from_g(int64_t K, sag_dtype dt) { return dt == SAG_BF16 && K <= 256; }
 
 struct TnPlan {
-    int64_t n_kblk, n_nblk, chunks, rows_per_chunk;
+    int64_t tile_k, tile_n, n_kblk, n_nblk, chunks, rows_per_chunk, max_chunks;   // max_chunks: of up to M rows
 };
 
-// One workgroup of sixteen wavefronts a CU, of at least 128 rows.
-TnPlan tn_plan(int64_t M, int64_t K, int64_t N) {
+// Columns of a tile.
+int tn_cols(int64_t N, sag_dtype dt) { return dt == SAG_BF16 || N > 64 ? kTnN : (N > 32 ? 64 : 32); }
+
+// bf16: one workgroup of sixteen wavefronts a CU; fp32: two of four.  Chunks of
+// at least 128 rows.
+TnPlan tn_plan(int64_t M, int64_t K, int64_t N, sag_dtype dt) {
     TnPlan p;
-    p.n_kblk = cdiv(K, kTnK);
-    p.n_nblk = cdiv(N, kTnN);
-    int64_t want = cdiv(256, p.n_kblk * p.n_nblk);
-    const int64_t most = cdiv(M > 0 ? M : 1, 2 * kTnRows);
+    p.tile_k = dt == SAG_BF16 ? kTnK : kT32K;
+    p.tile_n = tn_cols(N, dt);
+    p.n_kblk = cdiv(K, p.tile_k);
+    p.n_nblk = cdiv(N, p.tile_n);
+    const int64_t tiles = p.n_kblk * p.n_nblk, rows = dt == SAG_BF16 ? kTnRows : kT32Rows;
+    int64_t want = dt == SAG_BF16 ? cdiv(256, tiles) : (tiles < 512 ? 512 / tiles : 1);
+    const int64_t most = cdiv(M > 0 ? M : 1, 128);
     if (want > most) want = most;
-    p.rows_per_chunk = round_up(cdiv(M > 0 ? M : 1, want), kTnRows);
+    p.max_chunks = want;
+    p.rows_per_chunk = round_up(cdiv(M > 0 ? M : 1, want), rows);
     p.chunks = cdiv(M, p.rows_per_chunk);
     return p;
 }
 
 struct BwdWs {
-    void *bp, *hi, *lo, *tn;
+    void *bp, *hi, *lo;
     float *part, *part_cs;
-    size_t tn_bytes, used;
+    size_t used;
     bool fits;
 };
 
@@ -954,16 +1082,10 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, sag_dtype dt, void* ws, size_t byt
     BwdWs w{};
     w.bp = c.take<char>(pack_bytes(N, K, dt));
     if (!dz_from_g(K, dt)) w.hi = c.take<char>(dense_bytes(M, N, dt));
-    if (dt == SAG_BF16) {
-        if (!dz_from_g(K, dt) && M >= kFineRows) w.lo = c.take<char>(dense_bytes(M, N, dt));
-        const TnPlan p = tn_plan(M, K, N);
-        w.part = c.take<float>(p.chunks * p.n_kblk * kTnK * p.n_nblk * kTnN);
-        w.part_cs = c.take<float>(p.chunks * p.n_nblk * kTnN);
-    } else {
-        w.tn_bytes = gemm_tn_ws_bytes(M, round_up(K, vec_elems(dt)), N, dt);
-        w.tn = c.take<char>(w.tn_bytes);
-        w.part = c.take<float>(K * N);   // dW when only db is wanted
-    }
+    if (dt == SAG_BF16 && !dz_from_g(K, dt) && M >= kFineRows) w.lo = c.take<char>(dense_bytes(M, N, dt));
+    const TnPlan p = tn_plan(M, K, N, dt);
+    w.part = c.take<float>(p.max_chunks * p.n_kblk * p.tile_k * p.n_nblk * p.tile_n);
+    w.part_cs = c.take<float>(p.max_chunks * p.n_nblk * p.tile_n);
     w.used = c.used();
     w.fits = c.fits();
     return w;
@@ -983,9 +1105,17 @@ sag_status launch_tn(const TnArgs& a, int64_t chunks, hipStream_t s) {
     return SAG_OK;
 }
 
+sag_status tn_join(const TnPlan& p, int64_t K, int64_t N, float scale, float* dW, float* db, const BwdWs& w, hipStream_t s) {
+    const int64_t total = (dW ? K * N : 0) + (db ? N : 0);
+    dense_tn_reduce<<<dim3(static_cast<unsigned>(cdiv(total, 64))), 256, 0, s>>>(
+        w.part, w.part_cs, p.chunks, K, N, p.n_kblk * p.tile_k, p.n_nblk * p.tile_n, scale, dW, db);
+    SAG_LAUNCH_CHECK();
+    return SAG_OK;
+}
+
 // bf16: dW and db from G and Z, or from stored hi and lo.
 sag_status tn_run(sag_act act, TnArgs a, bool from_g, float* dW, float* db, const BwdWs& w, hipStream_t s) {
-    const TnPlan p = tn_plan(a.M, a.K, a.N);
+    const TnPlan p = tn_plan(a.M, a.K, a.N, SAG_BF16);
     a.n_kblk = p.n_kblk; a.n_nblk = p.n_nblk; a.rows_per_chunk = p.rows_per_chunk;
     a.part = w.part; a.part_cs = db ? w.part_cs : nullptr;
     const bool exact = act == SAG_ACT_NONE || act == SAG_ACT_RELU;
@@ -1015,11 +1145,24 @@ sag_status tn_run(sag_act act, TnArgs a, bool from_g, float* dW, float* db, cons
         }
         SAG_TRY(st);
     }
-    const int64_t total = (dW ? a.K * a.N : 0) + (db ? a.N : 0);
-    dense_tn_reduce<<<dim3(static_cast<unsigned>(cdiv(total, 64))), 256, 0, s>>>(
-        w.part, w.part_cs, p.chunks, a.K, a.N, p.n_kblk * kTnK, p.n_nblk * kTnN, scale, dW, db);
-    SAG_LAUNCH_CHECK();
-    return SAG_OK;
+    return tn_join(p, a.K, a.N, scale, dW, db, w, s);
+}
+
+// fp32: dW and db from X and the stored dZ.
+sag_status tn32_run(Tn32Args a, float* dW, float* db, const BwdWs& w, hipStream_t s) {
+    const TnPlan p = tn_plan(a.M, a.K, a.N, SAG_F32);
+    a.n_kblk = p.n_kblk; a.n_nblk = p.n_nblk; a.rows_per_chunk = p.rows_per_chunk;
+    a.part = w.part; a.part_cs = db ? w.part_cs : nullptr;
+    TraceScope trace(trace_enabled() ? shape_name("dense_dw", "f32", a.M, a.K, a.N) : std::string(), s,
+                     4 * (a.M * a.K + a.M * a.N + a.K * a.N + a.N), 2 * a.M * a.K * a.N);
+    if (p.chunks) {
+        const unsigned grid = static_cast<unsigned>(p.chunks * p.n_kblk * p.n_nblk);
+        if (p.tile_n == 128) dense_tn32<2, 2><<<grid, 256, 0, s>>>(a);
+        else if (p.tile_n == 64) dense_tn32<1, 2><<<grid, 256, 0, s>>>(a);
+        else dense_tn32<1, 1><<<grid, 256, 0, s>>>(a);
+        SAG_LAUNCH_CHECK();
+    }
+    return tn_join(p, a.K, a.N, 1.f, dW, db, w, s);
 }
 
 template <class T>
@@ -1075,9 +1218,9 @@ sag_status backward_typed(int64_t M, const T* X, int64_t ldx, int64_t K, const T
         a.z = dw_from_g ? Z : lo; a.ldz = dw_from_g ? ldz : ldh;
         return tn_run(act, a, dw_from_g, dW, db, w, s);
     } else {
-        GemmA a;
-        a.a1 = X; a.lda1 = ldx; a.k1 = K; a.m1 = M;
-        return gemm_tn_run(M, N, a, hi, ldh, nullptr, 0, dW ? dW : w.part, N, db, dt, w.tn, w.tn_bytes, s);
+        Tn32Args a{};
+        a.x = X; a.ldx = ldx; a.z = hi; a.ldz = ldh; a.M = M; a.K = K; a.N = N;
+        return tn32_run(a, dW, db, w, s);
     }
 }
 

@@ -206,3 +206,23 @@ def test_drop_struct_layout_matches_the_header(tmp_path):
     subprocess.run(["gcc", "-std=c11", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
     assert got == [ctypes.sizeof(L.SagDrop)] + [getattr(L.SagDrop, n).offset for n in fields]
+
+
+@pytest.mark.parametrize("dt", [L.SAG_F32, L.SAG_BF16])
+def test_a_workspace_for_many_rows_serves_fewer(dt):
+    lib = L.lib()
+    rows = sorted({1, 2, 63, 64, 65, 1000, 16383, 16384, 32767, 32768, 33000, 2 ** 20, 2 ** 24 + 1}
+                  | {int(1.07 ** i) for i in range(1, 250)})
+
+    def grows(f):
+        sizes = [f(m) for m in rows]
+        bad = [(a, x, b, y) for a, x, b, y in zip(rows, sizes, rows[1:], sizes[1:]) if y < x]
+        assert not bad, bad[:3]
+
+    for k, n in ((1, 1), (100, 47), (256, 256), (257, 300), (1500, 2000)):
+        grows(lambda m: lib.sag_dense_forward_workspace_bytes(m, k, n, dt))
+        if dt == L.SAG_BF16:       # (fp32 takes the plain product's workspace, for the size it is asked for)
+            grows(lambda m: lib.sag_dense_backward_workspace_bytes(m, k, n, dt))
+    for d, groups, graphs in ((1, 1, 1), (100, 10, 7), (256, 8, 600), (1000, 1, 5000), (64, 64, 1)):
+        grows(lambda m: lib.sag_group_norm_forward_workspace_bytes(m, d, groups, graphs, dt))
+        grows(lambda m: lib.sag_group_norm_backward_workspace_bytes(m, d, groups, graphs, dt))

@@ -175,3 +175,80 @@ def test_activations_of_infinity(dt, rows):
         assert (y[1] == np.inf).all() and np.isnan(y[3]).all() and np.isfinite(np.delete(y, [1, 2, 3], 0)).all(), kind
         if kind in ("relu", "gelu"):
             assert (y[2] == 0).all(), kind
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("graphs", [0, 1, 600])
+def test_norm_without_rows(dt, graphs):
+    say(f"norm no rows {dt} graphs={graphs}")
+    X = sag.empty_dense(0, 40, tb.TD[dt], DEV)
+    seg = to_dev(np.zeros(graphs + 1, np.int64))
+    w = torch.full((40,), 2.0, device=DEV)
+    out, ctx = sag.group_norm_forward(X, 4, w, seg=seg, eps=0.25, act="gelu")
+    assert out.shape == (0, 40) and ctx.mean.shape == (graphs, 4)
+    assert not f64(ctx.mean).any() and np.all(f64(ctx.rstd) == 2.0)
+    dw, db, dX = sag.group_norm_backward(ctx, X)
+    assert dX.shape == (0, 40) and not f64(dw).any() and not f64(db).any()
+
+
+def test_norm_of_rows_in_no_graph():
+    """Rows before the first graph and behind the last of many, with NaN in
+    them, stay as they were in Out and in dX and count nowhere."""
+    say("norm rows in no graph")
+    g = np.random.default_rng(20)
+    n, d = 6000, 32
+    X, G = tb.mat(g, n, d, "bf16"), tb.mat(g, n, d, "bf16")
+    seg = np.sort(g.integers(50, n - 70, 601)).astype(np.int64)
+    lo, hi = int(seg[0]), int(seg[-1])
+    want, c0 = sag.group_norm_forward(X, 4, seg=to_dev(seg), act="silu")
+    w0, b0, x0 = sag.group_norm_backward(c0, G)
+    X[:lo], X[hi:], G[:lo], G[hi:] = (float("nan"),) * 4
+    out, dX = (sag.empty_dense(n, d, torch.bfloat16, DEV, fill=3.0) for _ in range(2))
+    _, ctx = sag.group_norm_forward(X, 4, seg=to_dev(seg), act="silu", Out=out)
+    dw, db, _ = sag.group_norm_backward(ctx, G, dX=dX)
+    for a, b in ((out, want), (dX, x0)):
+        assert np.array_equal(tb.raw(a[lo:hi]), tb.raw(b[lo:hi])) and (f64(a[:lo]) == 3).all() and (f64(a[hi:]) == 3).all()
+    assert np.array_equal(tb.raw(dw), tb.raw(w0)) and np.array_equal(tb.raw(db), tb.raw(b0))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_large_calls_in_a_graph_and_in_one_workspace(dt):
+    """The tiled kernels and wavefronts' graphs captured, replayed with a mask
+    that advances and eager work between, and two calls one after the other in
+    one workspace: equal to eager calls with workspaces of their own."""
+    say(f"large calls captured {dt}")
+    g = np.random.default_rng(21)
+    M, K, N = 5000, 100, 136
+    X, R, G = tb.mat(g, M, K, dt), tb.mat(g, M, N, dt), tb.mat(g, M, N, dt)
+    W = tb.mat(g, K, N, dt, scale=0.1).contiguous()
+    seg = to_dev(np.asarray(tb.cuts(M, 700, 9), np.int64))
+    counter = torch.zeros(1, dtype=torch.int32, device=DEV)
+    drop = sag.Drop(0.3, 5, counter=counter)
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+
+    def run(ws=None):
+        out, z, ctx = sag.dense_layer_forward(X, W, act="gelu", drop=drop, residual=R, ws=ws)
+        y, nctx = sag.group_norm_forward(out, 4, seg=seg, act="silu", ws=ws)
+        dw, db, dy = sag.group_norm_backward(nctx, G, ws=ws)
+        dW, dc, dX = sag.dense_layer_backward(ctx, z, dy, ws=ws)
+        return y, dw, db, dW, dc, dX
+
+    want = []
+    for c in range(3):
+        counter.fill_(c)
+        want.append([tb.raw(t).copy() for t in run()])
+        assert all(np.array_equal(a, tb.raw(b)) for a, b in zip(want[-1], run(ws)))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(ws)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(ws)
+    for c in (0, 2, 1, 0, 2):
+        counter.fill_(c)
+        torch.randn(1000, device=DEV).sum()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(a, tb.raw(b)) for a, b in zip(want[c], outs)), c
