@@ -621,7 +621,8 @@ sag_status sag_gemm_tn(int64_t M, int64_t N, const void* A1, int64_t lda1, int64
  * with node ids for stream ids every partition drops the same elements of a
  * node's row.  call = `call` plus, where call_dev is given, the word it points
  * to (device uint32) when the kernel runs, modulo 2^32: a captured graph
- * draws a new mask at each replay once the caller advances that word.
+ * draws a new mask at each replay once the caller advances that word (not
+ * between a forward pass and its backward).
  * The mask depends on nothing else (not on ld, dtype, width or which entry
  * point applies it), so the backward pass recomputes it from the same
  * description.  The struct is read during the call only. */

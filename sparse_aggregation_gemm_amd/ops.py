@@ -847,7 +847,8 @@ class Drop:
     (taken to the nearest 2^-16), the generator's seed and call number, the
     stream ids of the rows (nodes: int32 [rows] on the device; None: row0 + r)
     and, for captured graphs, a device word (counter: int32 or uint32 [1])
-    added to `call` when the kernel runs."""
+    added to `call` when the kernel runs: advance it between steps, not between
+    a forward pass and its backward, which draws the same mask again."""
     p: float
     seed: int
     call: int = 0

@@ -252,3 +252,39 @@ def test_large_calls_in_a_graph_and_in_one_workspace(dt):
         graph.replay()
         torch.cuda.synchronize()
         assert all(np.array_equal(a, tb.raw(b)) for a, b in zip(want[c], outs)), c
+
+
+def test_rows_past_32_bits():
+    """4.6 G elements a matrix: the last rows come out as they do in a call of
+    their own (small whole numbers, so that every sum is exact; group norm
+    within a step of bf16, as its sums are cut elsewhere)."""
+    say("rows past 32 bits")
+    n, d, m = 2 ** 24 + 2 ** 20 + 5, 256, 3001
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of free memory")
+
+    def tail(seed):
+        g = np.random.default_rng(seed)
+        small = tb.mat(g, m, d, "bf16", True)
+        big = torch.zeros(n, d, dtype=torch.bfloat16, device=DEV)
+        big[n - m:] = small
+        return big, small
+
+    (X, x), (G, g) = tail(30), tail(31)
+    W = tb.mat(np.random.default_rng(32), d, d, "bf16", True).contiguous()
+    far, near = sag.Drop(0.5, 3, row0=5), sag.Drop(0.5, 3, row0=5 + n - m)
+    assert np.array_equal(tb.raw(sag.dropout(X, far)[n - m:]), tb.raw(sag.dropout(x, near)))
+    out, z, ctx = sag.dense_layer_forward(X, W, act="relu", drop=far, residual=G)
+    o, y, c = sag.dense_layer_forward(x, W, act="relu", drop=near, residual=g)
+    assert np.array_equal(tb.raw(out[n - m:]), tb.raw(o)) and np.array_equal(tb.raw(z[n - m:]), tb.raw(y))
+    del out
+    for a, b in zip(sag.dense_layer_backward(ctx, z, G), sag.dense_layer_backward(c, y, g)):
+        assert np.array_equal(tb.raw(a[n - m:] if a.shape[0] == n else a), tb.raw(b))
+    del z, ctx
+    seg = np.array([0, 7, n - m, n - m + 20, n], np.int64)
+    out, ctx = sag.group_norm_forward(X, 8, seg=to_dev(seg), act="none")
+    o, c = sag.group_norm_forward(x, 8, seg=to_dev(np.array([0, 20, m], np.int64)), act="none")
+    tb.within(out[n - m:], f64(o), 2.0 ** -7 * np.abs(f64(o)) + 1e-6)
+    got, want = sag.group_norm_backward(ctx, G), sag.group_norm_backward(c, g)
+    # (a step of bf16 of each value, and where terms cancel 2^-20 of their size)
+    tb.within(got[2][n - m:], f64(want[2]), 2.0 ** -7 * np.abs(f64(want[2])) + 1e-4)
